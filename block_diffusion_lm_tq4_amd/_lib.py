@@ -69,6 +69,22 @@ SIGNATURES = {
     "tq4_moe_grouped_fp8_workspace_size": (_SZ, [_I64, _I32, _I32, _I64, _I64]),
     "tq4_moe_grouped_fp8": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I32, _I32, _P, _I64, _P,
                                            _P, _P, _SZ, _P]),
+    "tq4_int8_cache_size": (_SZ, [_I64, _I64]),
+    "tq4_int8_cache": (ctypes.c_int, [_P, _I64, _I64, _U32, _P, _P]),
+    "tq4_int8_cache_bf16": (ctypes.c_int, [_P, _I64, _I64, _P, _P]),
+    "tq4_act_int8": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P]),
+    "tq4_linear_int8_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "tq4_linear_int8": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _P, _P, _SZ, _P]),
+    "tq4_linear_int8_epilogue": (ctypes.c_int,
+                                 [_P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "tq4_linear_int8_epilogue_bf16": (ctypes.c_int,
+                                      [_P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "tq4_linear_int8_quantized": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I64, _P, _P]),
+    "tq4_moe_grouped_int8_workspace_size": (_SZ, [_I64, _I32, _I32, _I64, _I64]),
+    "tq4_moe_grouped_int8": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I32, _I32, _P, _I64, _P,
+                                            _P, _P, _SZ, _P]),
+    "tq4_moe_router_scored": (ctypes.c_int, [_P, _I64, _I32, _I32, ctypes.c_int, _P, _I32, _I32,
+                                             ctypes.c_int, ctypes.c_float, _P, _P, _P]),
     "tq4_moe_router": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P]),
     "tq4_read_probe": (ctypes.c_int, [_P, _I64, _P, _P]),
 }

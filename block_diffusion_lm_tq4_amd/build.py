@@ -33,6 +33,8 @@ SOURCES = {
     "moe.hip": [],
     "probe.hip": [],
     "fp8.hip": ["-ffp-contract=off"],
+    "int8.hip": ["-ffp-contract=off"],
+    "router.hip": ["-ffp-contract=off"],
 }
 
 ARCH = "gfx950"

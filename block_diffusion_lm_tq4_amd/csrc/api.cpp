@@ -101,7 +101,7 @@ const char *tq4_status_string(int status) {
   }
 }
 
-int tq4_version(void) { return 100; }
+int tq4_version(void) { return 200; }
 
 int tq4_codebook(float *out) {
   if (out == nullptr) return TQ4_E_NULL;
@@ -157,12 +157,8 @@ size_t tq4_linear_workspace_size(int64_t m, int64_t k, int64_t n) {
 
 namespace {
 
-// Argument checks of the linear layer; none touches the device.  TQ4_OK means
-// the call may proceed (it is then a no-op if m or n is 0).
-int linear_args(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *packed, int64_t n,
-                const tq4::Tail &tail, const void *y) {
-  if (m < 0 || k < 0 || n < 0 || k % 32 != 0) return TQ4_E_SHAPE;
-  if (m == 0 || n == 0) return TQ4_OK;
+// Checks of a linear layer's output and tail (m, n > 0).
+int linear_tail_args(int64_t m, int64_t n, const tq4::Tail &tail, const void *y) {
   if (y == nullptr) return TQ4_E_NULL;
   const size_t elem = tail.bf16 ? 2 : 4;
   if (!aligned(y, elem) || !aligned(tail.bias, 4) || !aligned(tail.residual, elem))
@@ -174,6 +170,17 @@ int linear_args(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *pac
     const uintptr_t bytes = static_cast<uintptr_t>(m) * static_cast<uintptr_t>(n) * elem;
     if (r0 < y0 + bytes && y0 < r0 + bytes) return TQ4_E_SHAPE;
   }
+  return TQ4_OK;
+}
+
+// Argument checks of the linear layer; none touches the device.  TQ4_OK means
+// the call may proceed (it is then a no-op if m or n is 0).
+int linear_args(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *packed, int64_t n,
+                const tq4::Tail &tail, const void *y) {
+  if (m < 0 || k < 0 || n < 0 || k % 32 != 0) return TQ4_E_SHAPE;
+  if (m == 0 || n == 0) return TQ4_OK;
+  const int st = linear_tail_args(m, n, tail, y);
+  if (st != TQ4_OK) return st;
   if (k == 0) return TQ4_OK;
   if (x_bf16 == nullptr || packed == nullptr) return TQ4_E_NULL;
   if (!aligned(x_bf16, 16) || !aligned(packed, 4)) return TQ4_E_ALIGN;
@@ -635,6 +642,272 @@ int tq4_moe_grouped_fp8(const uint16_t *x_bf16, int64_t t, int64_t k, const int3
                             tiles, meta, l.max_tiles, o, nullptr, nullptr, s);
   if (e == hipSuccess) e = tq4::launch_combine(o, inv, topk_w, t, topk, k, out, s);
   return device_status(e);
+}
+
+// ---- int8 products --------------------------------------------------------
+
+namespace {
+
+// int32 sums of 127^2 stay below 2^31 up to this k
+constexpr int64_t kI8MaxK = 131072;
+
+bool int8_sizes_ok(int64_t rows, int64_t k) {
+  return rows >= 0 && rows <= INT32_MAX && k >= 0 && k % 32 == 0 && k <= kI8MaxK;
+}
+
+size_t int8_codes_bytes(int64_t rows, int64_t k) {
+  return static_cast<size_t>(rows) * static_cast<size_t>(tq4::int8_padded_k(k));
+}
+
+const float *int8_scales(const uint8_t *cache, int64_t rows, int64_t k) {
+  return reinterpret_cast<const float *>(cache + int8_codes_bytes(rows, k));
+}
+
+int linear_int8_impl(const uint16_t *x_bf16, const int8_t *x_codes, const float *x_scales,
+                     int64_t m, int64_t k, const uint8_t *cache, int64_t n,
+                     const tq4::Tail &tail, void *y, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+  if (!int8_sizes_ok(m, k) || !int8_sizes_ok(n, k)) return TQ4_E_SHAPE;
+  if (m == 0 || n == 0) return TQ4_OK;
+  const int st = linear_tail_args(m, n, tail, y);
+  if (st != TQ4_OK) return st;
+  hipStream_t s = as_stream(stream);
+  float *yf = static_cast<float *>(y);
+  const bool plain = tail.bias == nullptr && tail.residual == nullptr && !tail.bf16;
+  if (k == 0)
+    return device_status(plain ? tq4::launch_fill_zero(yf, m * n, s)
+                               : tq4::launch_tail_only(tail, m, n, yf, s));
+  if (cache == nullptr) return TQ4_E_NULL;
+  if (!aligned(cache, 16)) return TQ4_E_ALIGN;
+  if (x_bf16 != nullptr) {
+    if (!aligned(x_bf16, 16)) return TQ4_E_ALIGN;
+    const int ws = check_workspace(workspace, workspace_bytes,
+                                   tq4_linear_int8_workspace_size(m, k, n));
+    if (ws != TQ4_OK) return ws;
+    int8_t *xq = static_cast<int8_t *>(workspace);
+    float *xs = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                          align_up(int8_codes_bytes(m, k)));
+    const hipError_t e = tq4::launch_act_int8(x_bf16, m, k, xq, xs, s);
+    if (e != hipSuccess) return TQ4_E_DEVICE;
+    x_codes = xq;
+    x_scales = xs;
+  } else {
+    if (x_codes == nullptr || x_scales == nullptr) return TQ4_E_NULL;
+    if (!aligned(x_codes, 16) || !aligned(x_scales, 4)) return TQ4_E_ALIGN;
+  }
+  return device_status(tq4::launch_linear_int8(x_codes, x_scales, m, k,
+                                               reinterpret_cast<const int8_t *>(cache),
+                                               int8_scales(cache, n, k), n, tail, y, s));
+}
+
+// A call that is given bf16 rows needs them wherever it reads them.
+int linear_int8_bf16(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache,
+                     int64_t n, const tq4::Tail &tail, void *y, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+  if (x_bf16 == nullptr && m > 0 && n > 0 && k > 0 && int8_sizes_ok(m, k) && int8_sizes_ok(n, k))
+    return TQ4_E_NULL;
+  return linear_int8_impl(x_bf16, nullptr, nullptr, m, k, cache, n, tail, y, workspace,
+                          workspace_bytes, stream);
+}
+
+}  // namespace
+
+size_t tq4_int8_cache_size(int64_t n, int64_t k) {
+  if (!int8_sizes_ok(n, k) || k == 0) return 0;
+  return int8_codes_bytes(n, k) + static_cast<size_t>(n) * sizeof(float);
+}
+
+int tq4_int8_cache(const uint8_t *packed, int64_t n, int64_t k, uint32_t sign_bits,
+                   uint8_t *cache, void *stream) {
+  if (!int8_sizes_ok(n, k)) return TQ4_E_SHAPE;
+  if (n == 0 || k == 0) return TQ4_OK;
+  if (packed == nullptr || cache == nullptr) return TQ4_E_NULL;
+  if (!aligned(packed, 4) || !aligned(cache, 16)) return TQ4_E_ALIGN;
+  return device_status(tq4::launch_int8_cache(
+      packed, n, k, sign_bits, reinterpret_cast<int8_t *>(cache),
+      const_cast<float *>(int8_scales(cache, n, k)), as_stream(stream)));
+}
+
+int tq4_int8_cache_bf16(const uint16_t *w_bf16, int64_t n, int64_t k, uint8_t *cache,
+                        void *stream) {
+  if (!int8_sizes_ok(n, k)) return TQ4_E_SHAPE;
+  if (n == 0 || k == 0) return TQ4_OK;
+  if (w_bf16 == nullptr || cache == nullptr) return TQ4_E_NULL;
+  if (!aligned(w_bf16, 16) || !aligned(cache, 16)) return TQ4_E_ALIGN;
+  return device_status(tq4::launch_act_int8(w_bf16, n, k, reinterpret_cast<int8_t *>(cache),
+                                            const_cast<float *>(int8_scales(cache, n, k)),
+                                            as_stream(stream)));
+}
+
+int tq4_act_int8(const uint16_t *x_bf16, int64_t m, int64_t k, int8_t *codes, float *scales,
+                 void *stream) {
+  if (!int8_sizes_ok(m, k)) return TQ4_E_SHAPE;
+  if (m == 0 || k == 0) return TQ4_OK;
+  if (x_bf16 == nullptr || codes == nullptr || scales == nullptr) return TQ4_E_NULL;
+  if (!aligned(x_bf16, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return TQ4_E_ALIGN;
+  return device_status(tq4::launch_act_int8(x_bf16, m, k, codes, scales, as_stream(stream)));
+}
+
+size_t tq4_linear_int8_workspace_size(int64_t m, int64_t k, int64_t n) {
+  if (!int8_sizes_ok(m, k) || !int8_sizes_ok(n, k)) return 0;
+  if (m == 0 || n == 0 || k == 0) return 0;
+  return align_up(int8_codes_bytes(m, k)) + align_up(static_cast<size_t>(m) * sizeof(float));
+}
+
+int tq4_linear_int8(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache,
+                    int64_t n, float *y, void *workspace, size_t workspace_bytes, void *stream) {
+  return linear_int8_bf16(x_bf16, m, k, cache, n, tq4::Tail{}, y, workspace, workspace_bytes,
+                          stream);
+}
+
+int tq4_linear_int8_epilogue(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache,
+                             int64_t n, const float *bias, const float *residual, float *y,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+  return linear_int8_bf16(x_bf16, m, k, cache, n, tq4::Tail{bias, residual, 0}, y, workspace,
+                          workspace_bytes, stream);
+}
+
+int tq4_linear_int8_epilogue_bf16(const uint16_t *x_bf16, int64_t m, int64_t k,
+                                  const uint8_t *cache, int64_t n, const float *bias,
+                                  const uint16_t *residual_bf16, uint16_t *y_bf16,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+  return linear_int8_bf16(x_bf16, m, k, cache, n, tq4::Tail{bias, residual_bf16, 1}, y_bf16,
+                          workspace, workspace_bytes, stream);
+}
+
+int tq4_linear_int8_quantized(const int8_t *x_codes, const float *x_scales, int64_t m, int64_t k,
+                              const uint8_t *cache, int64_t n, float *y, void *stream) {
+  return linear_int8_impl(nullptr, x_codes, x_scales, m, k, cache, n, tq4::Tail{}, y, nullptr, 0,
+                          stream);
+}
+
+namespace {
+
+struct MoEInt8Layout {
+  int tile_rows;
+  int64_t max_tiles;
+  size_t counts, offsets, perm, inv, tiles, meta, xq, xs, h, hq, hs, o, total;
+};
+
+MoEInt8Layout moe_int8_layout(int64_t t, int32_t topk, int32_t e, int64_t n1, int64_t k) {
+  const int64_t pairs = t * topk;
+  MoEInt8Layout l{};
+  l.tile_rows = tq4::int8_moe_tile_rows(pairs, e);
+  const int64_t busy = pairs < e ? pairs : e;
+  l.max_tiles = pairs / l.tile_rows + busy + 1;
+  const size_t p = static_cast<size_t>(pairs);
+  size_t off = 0;
+  l.counts = off;  off += align_up(sizeof(int32_t) * e);
+  l.offsets = off; off += align_up(sizeof(int32_t) * (e + 1));
+  l.perm = off;    off += align_up(sizeof(int32_t) * p);
+  l.inv = off;     off += align_up(sizeof(int32_t) * p);
+  l.tiles = off;   off += align_up(sizeof(MoETile) * static_cast<size_t>(l.max_tiles));
+  l.meta = off;    off += kAlign;
+  l.xq = off;      off += align_up(int8_codes_bytes(t, k));
+  l.xs = off;      off += align_up(static_cast<size_t>(t) * sizeof(float));
+  l.h = off;       off += align_up(p * static_cast<size_t>(n1) * 2);
+  l.hq = off;      off += align_up(int8_codes_bytes(pairs, n1));
+  l.hs = off;      off += align_up(p * sizeof(float));
+  l.o = off;       off += align_up(p * static_cast<size_t>(k) * 4);
+  l.total = off;
+  return l;
+}
+
+bool moe_int8_shape_ok(int64_t t, int32_t topk, int32_t e, int64_t n1, int64_t k) {
+  if (t < 0 || t > INT32_MAX || topk < 1 || e < 1 || e > 512 || topk > e) return false;
+  if (n1 <= 0 || k <= 0 || !int8_sizes_ok(1, n1) || !int8_sizes_ok(1, k)) return false;
+  // 32-bit offsets into the code arrays
+  if (t * tq4::int8_padded_k(k) > INT32_MAX || t * topk > INT32_MAX ||
+      t * topk * tq4::int8_padded_k(n1) > INT32_MAX)
+    return false;
+  return moe_int8_layout(t, topk, e, n1, k).max_tiles <= 65535;
+}
+
+}  // namespace
+
+size_t tq4_moe_grouped_int8_workspace_size(int64_t t, int32_t topk, int32_t n_experts,
+                                           int64_t n1, int64_t k) {
+  if (!moe_int8_shape_ok(t, topk, n_experts, n1, k)) return 0;
+  return moe_int8_layout(t, topk, n_experts, n1, k).total;
+}
+
+int tq4_moe_grouped_int8(const uint16_t *x_bf16, int64_t t, int64_t k, const int32_t *topk_ids,
+                         const float *topk_w, int32_t topk, int32_t n_experts,
+                         const uint8_t *w1_cache, int64_t n1, const uint8_t *w2_cache, float *out,
+                         void *workspace, size_t workspace_bytes, void *stream) {
+  if (!moe_int8_shape_ok(t, topk, n_experts, n1, k)) return TQ4_E_SHAPE;
+  if (t == 0) return TQ4_OK;
+  if (x_bf16 == nullptr || topk_ids == nullptr || topk_w == nullptr || w1_cache == nullptr ||
+      w2_cache == nullptr || out == nullptr)
+    return TQ4_E_NULL;
+  if (!aligned(x_bf16, 16) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+      !aligned(w1_cache, 16) || !aligned(w2_cache, 16) || !aligned(out, 16))
+    return TQ4_E_ALIGN;
+  const MoEInt8Layout l = moe_int8_layout(t, topk, n_experts, n1, k);
+  if (workspace == nullptr || workspace_bytes < l.total) return TQ4_E_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return TQ4_E_ALIGN;
+  char *ws = static_cast<char *>(workspace);
+  int32_t *counts = reinterpret_cast<int32_t *>(ws + l.counts);
+  int32_t *offsets = reinterpret_cast<int32_t *>(ws + l.offsets);
+  int32_t *perm = reinterpret_cast<int32_t *>(ws + l.perm);
+  int32_t *inv = reinterpret_cast<int32_t *>(ws + l.inv);
+  MoETile *tiles = reinterpret_cast<MoETile *>(ws + l.tiles);
+  int32_t *meta = reinterpret_cast<int32_t *>(ws + l.meta);
+  int8_t *xq = reinterpret_cast<int8_t *>(ws + l.xq);
+  float *xs = reinterpret_cast<float *>(ws + l.xs);
+  uint16_t *h = reinterpret_cast<uint16_t *>(ws + l.h);
+  int8_t *hq = reinterpret_cast<int8_t *>(ws + l.hq);
+  float *hs = reinterpret_cast<float *>(ws + l.hs);
+  float *o = reinterpret_cast<float *>(ws + l.o);
+  const int64_t pairs = t * topk;
+  const int64_t e64 = n_experts;
+  hipStream_t s = as_stream(stream);
+  hipError_t e = tq4::launch_act_int8(x_bf16, t, k, xq, xs, s);
+  if (e == hipSuccess)
+    e = tq4::launch_route(topk_ids, pairs, topk, n_experts, counts, offsets, perm, inv, tiles,
+                          meta, l.tile_rows, nullptr, s);
+  if (e == hipSuccess)
+    e = tq4::launch_moe_int8(0, l.tile_rows, xq, xs, k, perm, topk,
+                             reinterpret_cast<const int8_t *>(w1_cache),
+                             int8_scales(w1_cache, e64 * n1, k), n1, tiles, meta, l.max_tiles, h,
+                             s);
+  if (e == hipSuccess) e = tq4::launch_act_int8(h, pairs, n1, hq, hs, s);
+  if (e == hipSuccess)
+    e = tq4::launch_moe_int8(1, l.tile_rows, hq, hs, n1, perm, topk,
+                             reinterpret_cast<const int8_t *>(w2_cache),
+                             int8_scales(w2_cache, e64 * k, n1), k, tiles, meta, l.max_tiles, o,
+                             s);
+  if (e == hipSuccess) e = tq4::launch_combine(o, inv, topk_w, t, topk, k, out, s);
+  return device_status(e);
+}
+
+int tq4_moe_router_scored(const float *logits, int64_t t, int32_t n_experts, int32_t topk,
+                          int score, const float *bias, int32_t n_groups, int32_t topk_groups,
+                          int renormalize, float scale, int32_t *topk_ids, float *topk_w,
+                          void *stream) {
+  if (t < 0 || n_experts < 1 || n_experts > 512 || topk < 1 || topk > n_experts)
+    return TQ4_E_SHAPE;
+  if (t > (int64_t{1} << 33)) return TQ4_E_SHAPE;  // grid of t / 4 workgroups
+  if (score != TQ4_SCORE_SOFTMAX && score != TQ4_SCORE_SIGMOID) return TQ4_E_SHAPE;
+  if (n_groups < 1 || n_experts % n_groups != 0 || topk_groups < 1 || topk_groups > n_groups)
+    return TQ4_E_SHAPE;
+  if (topk > topk_groups * (n_experts / n_groups)) return TQ4_E_SHAPE;
+  if (t == 0) return TQ4_OK;
+  if (logits == nullptr || topk_ids == nullptr || topk_w == nullptr) return TQ4_E_NULL;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+    return TQ4_E_ALIGN;
+  tq4::RouterConfig cfg{};
+  cfg.n_experts = n_experts;
+  cfg.topk = topk;
+  cfg.sigmoid = score == TQ4_SCORE_SIGMOID;
+  cfg.n_groups = n_groups;
+  // keeping every group is no choice
+  if (topk_groups == n_groups) cfg.n_groups = 1;
+  cfg.topk_groups = topk_groups == n_groups ? 1 : topk_groups;
+  cfg.renormalize = renormalize != 0;
+  cfg.scale = scale;
+  return device_status(
+      tq4::launch_router_scored(logits, t, cfg, bias, topk_ids, topk_w, as_stream(stream)));
 }
 
 int tq4_read_probe(const void *src, int64_t bytes, float *sink, void *stream) {

@@ -501,6 +501,250 @@ def moe_block_persistent(x: torch.Tensor, logits: torch.Tensor, topk: int,
     return out
 
 
+# ---------------------------------------------------------------------------
+# int8 products.  Scratch comes from torch's allocator on every call, so calls
+# on different streams, threads or captured graphs never share it.
+
+def _call(fn: str, dev: torch.device, *args) -> None:
+    """Run a C entry point on dev's current stream, with dev as the current device."""
+    if dev.index == torch.cuda.current_device():
+        check(fn, getattr(lib(), fn)(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn, getattr(lib(), fn)(*args, _stream(dev)))
+
+
+def _arg_on(t: torch.Tensor, name: str, dtype, dev: torch.device) -> None:
+    _cuda_contig(t, name, dtype)
+    _require(t.device == dev, f"{name} must be on {dev}")
+
+
+def _scratch(workspace: torch.Tensor | None, nbytes: int, dev: torch.device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _arg_on(workspace, "workspace", torch.uint8, dev)
+    return workspace
+
+
+def int8_padded_k(k: int) -> int:
+    return (k + 63) // 64 * 64
+
+
+def int8_cache_size(n: int, k: int) -> int:
+    return int(lib().tq4_int8_cache_size(n, k))
+
+
+def int8_cache(packed: torch.Tensor, sign_bits: int,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """packed [n, k/32, 20] -> the int8 weight cache (flat uint8: codes [n][kp],
+    then the n fp32 scales) (tq4_int8_cache)."""
+    _cuda_contig(packed, "packed", torch.uint8)
+    _require(packed.dim() == 3 and packed.shape[2] == BLOCK_BYTES, "packed must be [n, k/32, 20]")
+    n, k = packed.shape[0], packed.shape[1] * BLOCK
+    out = _int8_cache_out(out, n, k, packed.device)
+    _call("tq4_int8_cache", packed.device, packed.data_ptr(), n, k, sign_bits & 0xFFFFFFFF,
+          out.data_ptr())
+    return out
+
+
+def int8_cache_bf16(w: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """bf16 weights [n, k] -> the int8 weight cache (tq4_int8_cache_bf16)."""
+    _cuda_contig(w, "w", torch.bfloat16)
+    _require(w.dim() == 2, "w must be [n, k]")
+    n, k = w.shape
+    out = _int8_cache_out(out, n, k, w.device)
+    _call("tq4_int8_cache_bf16", w.device, w.data_ptr(), n, k, out.data_ptr())
+    return out
+
+
+def _int8_cache_out(out, n, k, dev):
+    size = int8_cache_size(n, k)
+    if out is None:
+        return torch.empty(size, dtype=torch.uint8, device=dev)
+    _arg_on(out, "out", torch.uint8, dev)
+    _require(out.numel() >= size, "out is smaller than tq4_int8_cache_size(n, k)")
+    return out
+
+
+def int8_cache_experts(packed: torch.Tensor, sign_bits: int) -> torch.Tensor:
+    """Experts' packed weights [E, n, k/32, 20] -> the int8 cache of the stacked
+    [E * n, k] matrix (the layout tq4_moe_grouped_int8 takes)."""
+    _require(packed.dim() == 4, "packed must be [E, n, k/32, 20]")
+    e, n, kb, bb = packed.shape
+    return int8_cache(packed.view(e * n, kb, bb), sign_bits)
+
+
+def int8_cache_views(cache: torch.Tensor, n: int, k: int) -> tuple[torch.Tensor, torch.Tensor]:
+    """(codes int8 [n, kp], scales fp32 [n]) views of a flat cache."""
+    kp = int8_padded_k(k)
+    return (cache[:n * kp].view(torch.int8).view(n, kp),
+            cache[n * kp:n * kp + 4 * n].view(torch.float32))
+
+
+def act_int8(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """bf16 x [m, k] -> (codes int8 [m, kp], scales fp32 [m]) (tq4_act_int8)."""
+    _cuda_contig(x, "x", torch.bfloat16)
+    _require(x.dim() == 2, "x must be [m, k]")
+    m, k = x.shape
+    codes = torch.empty((m, int8_padded_k(k)), dtype=torch.int8, device=x.device)
+    scales = torch.empty(m, dtype=torch.float32, device=x.device)
+    _call("tq4_act_int8", x.device, x.data_ptr(), m, k, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def linear_int8_workspace_size(m: int, k: int, n: int) -> int:
+    return int(lib().tq4_linear_int8_workspace_size(m, k, n))
+
+
+def _linear_int8(fn, x, cache, n, tail, out, workspace, ydtype):
+    _cuda_contig(x, "x", torch.bfloat16)
+    _require(x.dim() == 2, "x must be [m, k]")
+    m, k = x.shape
+    dev = x.device
+    _arg_on(cache, "cache", torch.uint8, dev)
+    _require(cache.numel() >= n * (int8_padded_k(k) + 4) or k == 0, "cache too small for [n, k]")
+    ptrs = []
+    if tail is not None:
+        bias, residual = tail
+        if bias is not None:
+            _arg_on(bias, "bias", torch.float32, dev)
+            _require(tuple(bias.shape) == (n,), "bias must be [n]")
+        if residual is not None:
+            _arg_on(residual, "residual", ydtype, dev)
+            _require(tuple(residual.shape) == (m, n), "residual must be [m, n]")
+        ptrs = [_ptr(bias), _ptr(residual)]
+    if out is None:
+        out = torch.empty((m, n), dtype=ydtype, device=dev)
+    else:
+        _arg_on(out, "out", ydtype, dev)
+        _require(tuple(out.shape) == (m, n), "out must be [m, n]")
+    workspace = _scratch(workspace, linear_int8_workspace_size(m, k, n), dev)
+    _call(fn, dev, x.data_ptr(), m, k, cache.data_ptr(), n, *ptrs, out.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def linear_int8(x: torch.Tensor, cache: torch.Tensor, n: int, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y = x . W^T in int8 from the cache of an [n, k] matrix, fp32 [m, n]
+    (tq4_linear_int8)."""
+    return _linear_int8("tq4_linear_int8", x, cache, n, None, out, workspace, torch.float32)
+
+
+def linear_int8_epilogue(x: torch.Tensor, cache: torch.Tensor, n: int,
+                         bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """linear_int8 + bias + residual, fp32 [m, n] (tq4_linear_int8_epilogue);
+    the residual may be `out` itself."""
+    return _linear_int8("tq4_linear_int8_epilogue", x, cache, n, (bias, residual), out, workspace,
+                        torch.float32)
+
+
+def linear_int8_epilogue_bf16(x: torch.Tensor, cache: torch.Tensor, n: int,
+                              bias: torch.Tensor | None = None,
+                              residual: torch.Tensor | None = None,
+                              out: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """bf16(linear_int8 + bias + residual), bf16 [m, n], the residual bf16
+    (tq4_linear_int8_epilogue_bf16); it may be `out` itself."""
+    return _linear_int8("tq4_linear_int8_epilogue_bf16", x, cache, n, (bias, residual), out,
+                        workspace, torch.bfloat16)
+
+
+def linear_int8_quantized(x_codes: torch.Tensor, x_scales: torch.Tensor, k: int,
+                          cache: torch.Tensor, n: int,
+                          out: torch.Tensor | None = None) -> torch.Tensor:
+    """y from activations already quantized by act_int8 (tq4_linear_int8_quantized)."""
+    _cuda_contig(x_codes, "x_codes", torch.int8)
+    dev = x_codes.device
+    _arg_on(x_scales, "x_scales", torch.float32, dev)
+    _arg_on(cache, "cache", torch.uint8, dev)
+    kp = int8_padded_k(k)
+    _require(x_codes.dim() == 2 and x_codes.shape[1] == kp, "x_codes must be [m, kp]")
+    m = x_codes.shape[0]
+    _require(tuple(x_scales.shape) == (m,), "x_scales must be [m]")
+    _require(cache.numel() >= n * (kp + 4) or k == 0, "cache too small for [n, k]")
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.float32, device=dev)
+    else:
+        _arg_on(out, "out", torch.float32, dev)
+        _require(tuple(out.shape) == (m, n), "out must be [m, n]")
+    _call("tq4_linear_int8_quantized", dev, x_codes.data_ptr(), x_scales.data_ptr(), m, k,
+          cache.data_ptr(), n, out.data_ptr())
+    return out
+
+
+def moe_grouped_int8_workspace_size(t: int, topk: int, n_experts: int, n1: int, k: int) -> int:
+    return int(lib().tq4_moe_grouped_int8_workspace_size(t, topk, n_experts, n1, k))
+
+
+def moe_grouped_int8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
+                     w1_cache: torch.Tensor, w2_cache: torch.Tensor, n_experts: int, n1: int,
+                     out: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The MoE layer on int8 expert caches (tq4_moe_grouped_int8); fp32 [t, k]."""
+    _cuda_contig(x, "x", torch.bfloat16)
+    _require(x.dim() == 2, "x must be [t, k]")
+    t, k = x.shape
+    dev = x.device
+    _arg_on(topk_ids, "topk_ids", torch.int32, dev)
+    _arg_on(topk_w, "topk_w", torch.float32, dev)
+    _arg_on(w1_cache, "w1_cache", torch.uint8, dev)
+    _arg_on(w2_cache, "w2_cache", torch.uint8, dev)
+    _require(topk_ids.dim() == 2 and topk_ids.shape[0] == t, "topk_ids must be [t, topk]")
+    topk = topk_ids.shape[1]
+    _require(tuple(topk_w.shape) == (t, topk), "topk_w must be [t, topk]")
+    _require(w1_cache.numel() >= n_experts * n1 * (int8_padded_k(k) + 4),
+             "w1_cache too small for [E * n1, k]")
+    _require(w2_cache.numel() >= n_experts * k * (int8_padded_k(n1) + 4),
+             "w2_cache too small for [E * k, n1]")
+    if out is None:
+        out = torch.empty((t, k), dtype=torch.float32, device=dev)
+    else:
+        _arg_on(out, "out", torch.float32, dev)
+        _require(tuple(out.shape) == (t, k), "out must be [t, k]")
+    workspace = _scratch(workspace, moe_grouped_int8_workspace_size(t, topk, n_experts, n1, k),
+                         dev)
+    _call("tq4_moe_grouped_int8", dev, x.data_ptr(), t, k, topk_ids.data_ptr(),
+          topk_w.data_ptr(), topk, n_experts, w1_cache.data_ptr(), n1, w2_cache.data_ptr(),
+          out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_router_scored(logits: torch.Tensor, topk: int, score: str = "softmax",
+                      bias: torch.Tensor | None = None, n_groups: int = 1, topk_groups: int = 1,
+                      renormalize: bool = False, scale: float = 1.0,
+                      ids: torch.Tensor | None = None, gates: torch.Tensor | None = None):
+    """The router with softmax or sigmoid scores, a balance bias, expert groups and
+    renormalized, scaled weights (tq4_moe_router_scored): (ids int32 [t, topk],
+    gates fp32 [t, topk]); slots without an expert have id -1 and gate 0."""
+    _cuda_contig(logits, "logits", torch.float32)
+    _require(logits.dim() == 2, "logits must be [t, n_experts]")
+    _require(score in SCORES, "score must be 'softmax' or 'sigmoid'")
+    t, e = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _arg_on(bias, "bias", torch.float32, dev)
+        _require(tuple(bias.shape) == (e,), "bias must be [n_experts]")
+    if ids is None:
+        ids = torch.empty((t, topk), dtype=torch.int32, device=dev)
+    else:
+        _arg_on(ids, "ids", torch.int32, dev)
+        _require(tuple(ids.shape) == (t, topk), "ids must be [t, topk]")
+    if gates is None:
+        gates = torch.empty((t, topk), dtype=torch.float32, device=dev)
+    else:
+        _arg_on(gates, "gates", torch.float32, dev)
+        _require(tuple(gates.shape) == (t, topk), "gates must be [t, topk]")
+    _call("tq4_moe_router_scored", dev, logits.data_ptr(), t, e, topk, SCORES[score], _ptr(bias),
+          n_groups, topk_groups, int(renormalize), float(scale), ids.data_ptr(), gates.data_ptr())
+    return ids, gates
+
+
 def read_probe(buf: torch.Tensor, sink: torch.Tensor) -> None:
     """One streaming read of a whole device buffer (tq4_read_probe), for timing."""
     _require(buf.is_cuda and buf.is_contiguous(), "buf must be a contiguous device tensor")

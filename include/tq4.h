@@ -313,6 +313,121 @@ int tq4_moe_grouped_fp8(const uint16_t *x_bf16, int64_t t, int64_t k,
                         const uint8_t *w2_cache, float *out, void *workspace,
                         size_t workspace_bytes, void *stream);
 
+/* ---- int8 products -------------------------------------------------------
+ * The layers on 8-bit integers (model card, Running it: the projections that
+ * every forward runs; Help wanted: a resident copy that no forward decodes):
+ * weights with one scale per output channel, activations with one scale per
+ * token, exact int32 sums.
+ *
+ * A row v[0..k) with a = max|v| is held as codes q_i = rint(127 * v_i / a)
+ * (ties to even, from the exact quotient) and the fp32 scale s = a / 127
+ * (correctly rounded); an all-zero row has zero codes and s = 0; a row
+ * holding a NaN or an infinity has zero codes and s = NaN.  Code rows are
+ * padded to kp = k rounded up to a multiple of 64 with zero codes.  A cache
+ * of an [n, k] matrix is the codes [n][kp] followed by the n scales (fp32).
+ * Sizes: rows up to 2^31 - 1, k a multiple of 32 up to 131072 (then no int32
+ * sum overflows).  Rows whose largest magnitude is below 127 * 2^-126 keep
+ * fewer bits of their scale. */
+
+/* Bytes of the int8 cache of an [n, k] matrix: n * kp + 4 * n (0 if the sizes
+ * are invalid or empty). */
+size_t tq4_int8_cache_size(int64_t n, int64_t k);
+
+/* Build the cache from a packed [n][k/32][20] matrix (device, 4-byte
+ * aligned): the decoded weights W_hat (rotation undone) held as above, the
+ * decoding and the quotients in fp64.  cache: device, 16-byte aligned,
+ * tq4_int8_cache_size bytes.  Offline, like tq4_pack.  Errors: TQ4_E_NULL,
+ * TQ4_E_SHAPE, TQ4_E_ALIGN, TQ4_E_DEVICE.  n == 0 or k == 0 is a no-op. */
+int tq4_int8_cache(const uint8_t *packed, int64_t n, int64_t k, uint32_t sign_bits,
+                   uint8_t *cache, void *stream);
+
+/* The same from BF16 weights [n, k] (device, 16-byte aligned; the form the
+ * checkpoint ships in).  Errors as tq4_int8_cache. */
+int tq4_int8_cache_bf16(const uint16_t *w_bf16, int64_t n, int64_t k, uint8_t *cache,
+                        void *stream);
+
+/* Quantize bf16 activations [m, k] (device, 16-byte aligned) as above: codes
+ * [m][kp] (device, 16-byte aligned) and scales [m] fp32 (device).  Errors as
+ * tq4_int8_cache. */
+int tq4_act_int8(const uint16_t *x_bf16, int64_t m, int64_t k, int8_t *codes, float *scales,
+                 void *stream);
+
+/* Workspace bytes for tq4_linear_int8 and its epilogue forms (the quantized
+ * activations). */
+size_t tq4_linear_int8_workspace_size(int64_t m, int64_t k, int64_t n);
+
+/* y[m, n] = (sum_k xq[m, k] wq[n, k]) * sx[m] * sw[n]: x quantized per call
+ * (tq4_act_int8, into the workspace), the weights from a cache built by
+ * tq4_int8_cache or tq4_int8_cache_bf16.  The sum is exact, the two products
+ * with the scales are fp32 in this order; deterministic.  Rows of x that hold
+ * a NaN or an infinity, and such rows of the weights, give NaN.
+ *   x_bf16 : [m, k] bf16 bit patterns, device, 16-byte aligned
+ *   cache  : for this [n, k], device, 16-byte aligned
+ *   y      : [m, n] fp32, device, 4-byte aligned, overwritten
+ *   workspace : tq4_linear_int8_workspace_size(m, k, n) bytes, 256-byte
+ *               aligned
+ * Errors: as tq4_linear.  m == 0 or n == 0 is a no-op; k == 0 writes zeros. */
+int tq4_linear_int8(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache,
+                    int64_t n, float *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* tq4_linear_int8 with the additive tail of tq4_linear_epilogue at the final
+ * store: + bias[n], then + residual[m, n], in fp32; either may be NULL, and
+ * the residual may be y itself.  With both NULL the result equals
+ * tq4_linear_int8's bit for bit.  Errors as tq4_linear_epilogue; k == 0 writes
+ * bias + residual. */
+int tq4_linear_int8_epilogue(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache,
+                             int64_t n, const float *bias, const float *residual, float *y,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same with a bf16 residual stream and bf16 output: the bf16 rounding of
+ * tq4_linear_int8_epilogue's fp32 result, bit for bit.  Arguments and errors
+ * as tq4_linear_epilogue_bf16. */
+int tq4_linear_int8_epilogue_bf16(const uint16_t *x_bf16, int64_t m, int64_t k,
+                                  const uint8_t *cache, int64_t n, const float *bias,
+                                  const uint16_t *residual_bf16, uint16_t *y_bf16,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* tq4_linear_int8 with the activations already quantized by tq4_act_int8
+ * (x_codes [m][kp], device, 16-byte aligned; x_scales [m], device, 4-byte
+ * aligned), so one quantization can serve several projections of the same
+ * input.  The codes behind k must be zero, as tq4_act_int8 leaves them.  No
+ * workspace.  Errors as tq4_linear_int8. */
+int tq4_linear_int8_quantized(const int8_t *x_codes, const float *x_scales, int64_t m, int64_t k,
+                              const uint8_t *cache, int64_t n, float *y, void *stream);
+
+/* Workspace bytes tq4_moe_grouped_int8 needs (0 if the sizes are invalid). */
+size_t tq4_moe_grouped_int8_workspace_size(int64_t t, int32_t topk, int32_t n_experts,
+                                           int64_t n1, int64_t k);
+
+/* The MoE layer of tq4_moe_grouped on int8 expert caches (model card, Running
+ * it: the sync-free MoE; The model underneath: 128 experts, top-6):
+ *   out[t, :] = sum_j topk_w[t, j] * dq(q(h_tj)) . dq(W2_e)^T,
+ *   h_tj = bf16(relu(u_tj)^2),  u_tj = dq(q(x[t, :])) . dq(W1_e)^T,
+ *   e = topk_ids[t, j],
+ * where q is the quantization of tq4_act_int8 and dq its value; ids outside
+ * [0, n_experts) contribute nothing (a token without any gets zeros).  u is
+ * formed from the exact integer sum and the two scales in fp64, its square
+ * rounded to fp32 and then to bf16, so the hidden codes do not depend on how
+ * the product was split; NaN rows stay NaN.
+ *   x_bf16   : [t, k] bf16 bit patterns, device, 16-byte aligned
+ *   topk_ids : [t, topk] int32, device;  topk_w : [t, topk] fp32, device
+ *   w1_cache : tq4_int8_cache of the experts' up projections stacked as one
+ *              [n_experts * n1, k] matrix (expert e = rows e*n1 ...), device,
+ *              16-byte aligned
+ *   w2_cache : the same for the down projections, [n_experts * k, n1]
+ *   out      : [t, k] fp32, device, 16-byte aligned, overwritten
+ *   workspace: tq4_moe_grouped_int8_workspace_size(...) bytes, device,
+ *              256-byte aligned, no initial contents required
+ * Steps: activation quantization, bucketing, grouped up projection with
+ * relu^2, quantization of the hidden rows, grouped down projection, and the
+ * per-token weighted sum in slot order (fp32).  Deterministic.  Errors: as
+ * tq4_moe_grouped, plus TQ4_E_SHAPE when t * kp or t * topk * n1p reach 2^31
+ * (kp, n1p: k, n1 padded to 64) or k or n1 exceed 131072. */
+int tq4_moe_grouped_int8(const uint16_t *x_bf16, int64_t t, int64_t k, const int32_t *topk_ids,
+                         const float *topk_w, int32_t topk, int32_t n_experts,
+                         const uint8_t *w1_cache, int64_t n1, const uint8_t *w2_cache, float *out,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
 /* Stable bucketing of the t*topk (token, slot) pairs by expert, the routing
  * step of the sync-free MoE (model card, Running it; 128 experts, top-6 in
  * The model underneath).  Pair p = token * topk + slot.
@@ -376,6 +491,40 @@ int tq4_moe_grouped(const uint16_t *x_bf16, int64_t t, int64_t k,
  * t == 0 is a no-op. */
 int tq4_moe_router(const float *logits, int64_t t, int32_t n_experts, int32_t topk,
                    int32_t *topk_ids, float *topk_w, void *stream);
+
+/* tq4_moe_router for the routers that balance their experts with a bias or
+ * limit a token to some groups of them (model card, The model underneath: the
+ * 128-expert, top-6 layer this stands in front of).  Per token t, with l =
+ * logits[t, :]:
+ *   p_e = softmax(l)_e (TQ4_SCORE_SOFTMAX) or 1 / (1 + exp(-l_e))
+ *         (TQ4_SCORE_SIGMOID);  c_e = p_e + bias[e] (p_e without a bias)
+ *   groups: group i is experts i * E/n_groups ... of E = n_experts; its value
+ *           is the sum of its two largest c; the topk_groups groups with the
+ *           largest values stay, ties to the lower group
+ *   topk_ids[t, :] = the topk largest c of the groups that stay, in decreasing
+ *           order, ties to the lower expert id
+ *   topk_w[t, j] = scale * p[topk_ids[t, j]], divided by the sum of the
+ *           token's chosen p if renormalize is not zero (0 if that sum is 0).
+ * Scores, comparisons and weights are fp64, the weights then rounded to fp32.
+ * An expert whose logit is -infinity or NaN, or whose c is, is switched off:
+ * it takes no part in the softmax and is never chosen; +infinity counts as
+ * the largest finite value.  A group without an expert left is never kept.
+ * Slots for which no expert is left get id -1 and weight 0, which the MoE
+ * layers above skip.
+ *   logits   : [t, n_experts] fp32, device
+ *   bias     : [n_experts] fp32, device, or NULL
+ *   topk_ids : [t, topk] int32, device, overwritten
+ *   topk_w   : [t, topk] fp32, device, overwritten
+ * Errors: TQ4_E_SHAPE (t < 0 or t > 2^33, n_experts outside 1..512, topk
+ * outside 1..topk_groups * (E / n_groups), n_groups not dividing E,
+ * topk_groups outside 1..n_groups, an unknown score), TQ4_E_NULL,
+ * TQ4_E_ALIGN (4-byte), TQ4_E_DEVICE.  t == 0 is a no-op. */
+#define TQ4_SCORE_SOFTMAX 0
+#define TQ4_SCORE_SIGMOID 1
+int tq4_moe_router_scored(const float *logits, int64_t t, int32_t n_experts, int32_t topk,
+                          int score, const float *bias, int32_t n_groups, int32_t topk_groups,
+                          int renormalize, float scale, int32_t *topk_ids, float *topk_w,
+                          void *stream);
 
 /* Workspace bytes tq4_moe_block needs (0 if the sizes are invalid). */
 size_t tq4_moe_block_workspace_size(int64_t t, int32_t topk, int32_t n_experts,

@@ -8,7 +8,9 @@ links it, and it shares no code, table or constant generator with that path.
 
 from .fp8_oracle import *  # noqa: F401,F403
 from .fp8_oracle import __all__ as _fp8_all
+from .int8_oracle import *  # noqa: F401,F403
+from .int8_oracle import __all__ as _int8_all
 from .tq4_oracle import *  # noqa: F401,F403
 from .tq4_oracle import __all__ as _tq4_all
 
-__all__ = list(_tq4_all) + list(_fp8_all)
+__all__ = list(_tq4_all) + list(_fp8_all) + list(_int8_all)

@@ -1,0 +1,568 @@
+"""GPU parity of the int8 layers and the scored router against the fp64 oracle.
+
+Codes and scales are compared bit for bit.  Products: the integer sums are
+exact; an output is then float(sum) * sx * sw, at most three roundings of half
+an fp32 step each (2^-24), plus one for each term of the tail, so each element
+must lie within
+    3.01 * 2^-24 |p| + 2^-24 (|p + b| + |p + b + r|) * 1.01
+of the oracle (p the product).  A bf16 output is the bf16 rounding of the fp32
+one, bit for bit.  The MoE layer's hidden codes are decided in fp64 on both
+sides, so its output is a sum of topk products g * o, each with at most four
+roundings, and topk adds: (topk + 5) * 2^-24 * sum |g o|.  Router ids are equal
+and its weights one rounding of fp64 values: 2^-24 relative (plus fp64's own).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from block_diffusion_lm_tq4_amd import inputs as I
+
+pytestmark = pytest.mark.gpu
+
+SB = I.sign_bits()
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from block_diffusion_lm_tq4_amd import ops  # noqa: F401  (loads libtq4.so)
+    return torch.device("cuda:0")
+
+
+def _ops():
+    from block_diffusion_lm_tq4_amd import ops
+    return ops
+
+
+def _bf16(bits, dev):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).to(dev).view(torch.bfloat16)
+
+
+def _acts(m, k, seed, gain=1.0):
+    x = gain * np.random.default_rng(seed).standard_normal((m, k))
+    x[:, ::max(1, k // 3)] *= 5.0
+    return O.bf16_bits_from_f32(x.astype(np.float32))
+
+
+def _weights(dev, n, k, seed):
+    """(cache on the device, codes, scales) of random bf16 weights."""
+    w = O.bf16_bits_from_f32(I.weights(n, k, seed=seed))
+    codes, scales = O.act_int8(w)
+    return _ops().int8_cache_bf16(_bf16(w, dev)), codes, scales
+
+
+def _views(cache, n, k):
+    codes, scales = _ops().int8_cache_views(cache, n, k)
+    return codes.cpu().numpy(), scales.cpu().numpy()
+
+
+def _same_bits(a, b):
+    return np.array_equal(np.asarray(a, np.float32).view(np.uint32),
+                          np.asarray(b, np.float32).view(np.uint32))
+
+
+# ---- codes -----------------------------------------------------------------
+
+@pytest.mark.parametrize("m,k", [(1, 32), (5, 96), (16, 2688), (300, 1856), (3, 8192), (1, 131072),
+                                 (2000, 64), (37, 4128)])
+def test_act_codes_equal_oracle(dev, m, k):
+    x = _acts(m, k, seed=m + k)
+    codes, scales = _ops().act_int8(_bf16(x, dev))
+    rc, rs = O.act_int8(x)
+    assert np.array_equal(codes.cpu().numpy()[:, :k], rc)
+    assert not codes.cpu().numpy()[:, k:].any()
+    assert _same_bits(scales.cpu().numpy(), rs)
+
+
+def test_act_codes_of_special_rows(dev):
+    k = 160
+    x = _acts(12, k, seed=4)
+    x[0] = 0                                     # all zero
+    x[1] = 0x8000                                # all minus zero
+    x[2, 77] = 0x7FC0                            # NaN
+    x[3, 159] = 0x7F80                           # infinity
+    x[4, 0] = 0xFF80                             # minus infinity
+    x[5] = 0x7F7F                                # the largest value, everywhere
+    x[5, 3] = 0x3F80
+    x[6] = np.arange(k) % 128                    # subnormals
+    x[7] = 0x0001
+    x[8, 1:] = 0x0080                            # a tiny row under one large value
+    x[8, 0] = 0x7F00
+    x[9] = (0x3F80 + np.arange(k) % 128)         # one binade: many near-ties
+    x[10] = (0x3F00 + np.arange(k))              # two binades against 127.0 / 64
+    x[10, 0] = 0x3FFE
+    x[11] |= 0x8000                              # all negative
+    codes, scales = _ops().act_int8(_bf16(x, dev))
+    rc, rs = O.act_int8(x)
+    assert np.array_equal(codes.cpu().numpy()[:, :k], rc)
+    got = scales.cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(rs))
+    assert _same_bits(got[~np.isnan(rs)], rs[~np.isnan(rs)])
+
+
+def test_act_codes_of_every_mantissa_pair(dev):
+    """Every bf16 mantissa under every largest mantissa, at 8 distances."""
+    man = np.arange(128, dtype=np.uint16)
+    rows = []
+    for top in range(128):
+        body = np.concatenate([0x4000 - 0x80 * d + man for d in range(1, 9)])
+        rows.append(np.concatenate([[0x4000 + top], 0x4000 + man[:top + 1],
+                                    np.zeros(127 - top, np.uint16), body,
+                                    np.zeros(31, np.uint16)]))
+    x = np.stack(rows).astype(np.uint16)
+    assert x.shape[1] % 32 == 0
+    codes, scales = _ops().act_int8(_bf16(x, dev))
+    rc, rs = O.act_int8(x)
+    assert np.array_equal(codes.cpu().numpy()[:, :x.shape[1]], rc)
+    assert _same_bits(scales.cpu().numpy(), rs)
+
+
+@pytest.mark.parametrize("n,k,kind", [(64, 256, "gaussian"), (40, 96, "student_t3"),
+                                      (33, 160, "gaussian"), (1024, 2688, "student_t3")])
+def test_cache_from_packed_equals_oracle(dev, n, k, kind):
+    w = I.weights(n, k, kind, seed=n + k)
+    p = O.pack(w, SB)
+    cache = _ops().int8_cache(torch.from_numpy(p).to(dev), SB)
+    codes, scales = _views(cache, n, k)
+    rc, rs = O.int8_cache_packed(p, SB)
+    assert np.array_equal(codes[:, :k], rc)
+    assert not codes[:, k:].any()
+    assert _same_bits(scales, rs)
+
+
+def test_cache_from_packed_special_rows(dev):
+    w = I.weights(4, 64, seed=5)
+    w[1] = 0
+    p = O.pack(w, SB)
+    p[2, 0, 16:18] = np.array([0x7F80], np.uint16).view(np.uint8)      # an infinite scale
+    p[3, 1, 18:20] = np.array([0x7FC0], np.uint16).view(np.uint8)      # a NaN scale
+    codes, scales = _views(_ops().int8_cache(torch.from_numpy(p).to(dev), SB), 4, 64)
+    rc, rs = O.int8_cache_packed(p[:2], SB)
+    assert np.array_equal(codes[:2], rc) and _same_bits(scales[:2], rs)
+    assert not codes[2:].any() and np.isnan(scales[2:]).all()
+
+
+# ---- the linear layer ------------------------------------------------------
+
+LINEAR = [(1, 32, 1), (1, 2688, 8192), (2, 64, 17), (3, 96, 33), (7, 1856, 130), (15, 2688, 48),
+          (16, 2688, 1000), (16, 8192, 257), (17, 160, 31), (31, 4096, 100), (33, 320, 511),
+          (48, 2688, 129), (64, 1856, 2688), (65, 2720, 70), (100, 96, 300), (127, 1024, 128),
+          (128, 2688, 256), (200, 352, 385), (255, 64, 513), (256, 2688, 640), (257, 1856, 1025),
+          (300, 8224, 260), (513, 128, 777), (1000, 2688, 1100)]
+
+
+def _check_linear(y, ref_p, bias=None, residual=None):
+    ref, tol = ref_p.copy(), 3.01 * U * np.abs(ref_p)
+    for extra in (None if bias is None else bias[None, :], residual):
+        if extra is not None:
+            ref = ref + extra
+            tol = tol + 1.01 * U * np.abs(ref)
+    err = np.abs(y.astype(np.float64) - ref)
+    assert (err <= tol + 1e-40).all(), (err - tol).max()
+
+
+@pytest.mark.parametrize("m,k,n", LINEAR)
+def test_linear_equals_oracle(dev, m, k, n):
+    x = _acts(m, k, seed=m)
+    cache, wc, ws = _weights(dev, n, k, seed=n)
+    xg = _bf16(x, dev)
+    rng = np.random.default_rng(m * 7 + n)
+    bias = rng.standard_normal(n).astype(np.float32)
+    r32 = rng.standard_normal((m, n)).astype(np.float32)
+    r16 = O.bf16_bits_from_f32(r32)
+    p = O.linear_int8(*O.act_int8(x), wc, ws)
+    y = _ops().linear_int8(xg, cache, n)
+    _check_linear(y.cpu().numpy(), p)
+    # an epilogue without terms is the plain call; the quantized form too
+    assert torch.equal(_ops().linear_int8_epilogue(xg, cache, n), y)
+    assert torch.equal(_ops().linear_int8_quantized(*_ops().act_int8(xg), k, cache, n), y)
+    bg, rg = torch.from_numpy(bias).to(dev), torch.from_numpy(r32).to(dev)
+    for b, r in ((bias, None), (None, r32), (bias, r32)):
+        z = _ops().linear_int8_epilogue(xg, cache, n, None if b is None else bg,
+                                        None if r is None else rg)
+        _check_linear(z.cpu().numpy(), p, b, r)
+    # bf16: the rounding of the fp32 form on the widened residual
+    rb = _bf16(r16, dev)
+    for b, r in ((None, None), (bg, None), (None, rb), (bg, rb)):
+        z32 = _ops().linear_int8_epilogue(xg, cache, n, b, None if r is None else r.float())
+        z16 = _ops().linear_int8_epilogue_bf16(xg, cache, n, b, r)
+        assert torch.equal(z16, z32.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("m", [1, 16, 40, 300])
+def test_linear_in_place_residual_and_guard(dev, m):
+    """The residual may be the output; nothing outside the output is written."""
+    k, n = 352, 200
+    cache, _, _ = _weights(dev, n, k, seed=1)
+    xg = _bf16(_acts(m, k, seed=2), dev)
+    for dt, fn in ((torch.float32, _ops().linear_int8_epilogue),
+                   (torch.bfloat16, _ops().linear_int8_epilogue_bf16)):
+        res = torch.randn(m, n, device=dev).to(dt)
+        ref = fn(xg, cache, n, None, res)
+        big = torch.full((m + 2, n), 7.0, dtype=dt, device=dev)
+        big[1:m + 1] = res
+        out = big[1:m + 1]
+        fn(xg, cache, n, None, out, out=out)
+        assert torch.equal(big[1:m + 1], ref)
+        assert (big[0] == 7).all() and (big[m + 1] == 7).all()
+
+
+@pytest.mark.parametrize("m", [3, 70, 300])
+def test_linear_nan_rows_and_channels(dev, m):
+    k, n = 192, 96
+    x = _acts(m, k, seed=3)
+    x[1, 5] = 0x7FC0
+    w = O.bf16_bits_from_f32(I.weights(n, k, seed=4))
+    w[7, 9] = 0x7F80
+    y = _ops().linear_int8(_bf16(x, dev), _ops().int8_cache_bf16(_bf16(w, dev)), n).cpu().numpy()
+    bad = np.zeros((m, n), bool)
+    bad[1] = True
+    bad[:, 7] = True
+    assert np.array_equal(np.isnan(y), bad)
+
+
+def test_linear_largest_sums(dev):
+    """k at its limit with every code at 127: the int32 sum is 127^2 k."""
+    k = 131072
+    one = torch.ones(2, k, dtype=torch.bfloat16, device=dev)
+    one[1] = -1
+    cache = _ops().int8_cache_bf16(torch.ones(48, k, dtype=torch.bfloat16, device=dev))
+    s = np.float32(1) / np.float32(127)
+    ref = np.float32(np.float32(127 * 127 * k) * s) * s
+    y = _ops().linear_int8(one, cache, 48).cpu().numpy()
+    assert (y[0] == ref).all() and (y[1] == -ref).all()
+    big = one[:1].expand(80, k).contiguous()
+    assert (_ops().linear_int8(big, cache, 48).cpu().numpy() == ref).all()
+
+
+def test_linear_empty(dev):
+    cache, _, _ = _weights(dev, 8, 64, seed=0)
+    x = torch.zeros(0, 64, dtype=torch.bfloat16, device=dev)
+    assert _ops().linear_int8(x, cache, 8).shape == (0, 8)
+    x = torch.zeros(3, 0, dtype=torch.bfloat16, device=dev)
+    empty = torch.empty(0, dtype=torch.uint8, device=dev)
+    assert (_ops().linear_int8(x, empty, 5) == 0).all()
+    b = torch.arange(5, dtype=torch.float32, device=dev)
+    assert torch.equal(_ops().linear_int8_epilogue(x, empty, 5, b), b.expand(3, 5))
+
+
+def test_linear_refusals(dev):
+    from block_diffusion_lm_tq4_amd._lib import TQ4Error
+    cache, _, _ = _weights(dev, 8, 64, seed=0)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device=dev)
+    with pytest.raises(ValueError, match="too small"):
+        _ops().linear_int8(x, cache, 9)
+    with pytest.raises(ValueError, match="contiguous"):
+        _ops().linear_int8(x[:, ::2], cache, 8)
+    with pytest.raises(ValueError, match="bfloat16"):
+        _ops().linear_int8(x.half(), cache, 8)
+    with pytest.raises(ValueError, match="residual"):
+        _ops().linear_int8_epilogue(x, cache, 8, None, torch.zeros(4, 9, device=dev))
+    with pytest.raises(TQ4Error, match="SHAPE"):
+        _ops().linear_int8(torch.zeros(4, 40, dtype=torch.bfloat16, device=dev), cache, 2)
+    with pytest.raises(TQ4Error, match="ALIGN"):
+        _ops().linear_int8(x, torch.zeros(2000, dtype=torch.uint8, device=dev)[4:], 8)
+    with pytest.raises(TQ4Error, match="WORKSPACE"):
+        _ops().linear_int8(x, cache, 8, workspace=torch.empty(8, dtype=torch.uint8, device=dev))
+
+
+# ---- the MoE layer ---------------------------------------------------------
+
+def _experts(dev, e, n1, k, seed):
+    rng = np.random.default_rng(seed)
+    w1 = O.bf16_bits_from_f32((0.05 * rng.standard_normal((e, n1, k))).astype(np.float32))
+    w2 = O.bf16_bits_from_f32((0.05 * rng.standard_normal((e, k, n1))).astype(np.float32))
+    c1 = _ops().int8_cache_bf16(_bf16(w1.reshape(e * n1, k), dev))
+    c2 = _ops().int8_cache_bf16(_bf16(w2.reshape(e * k, n1), dev))
+    return c1, c2, [O.act_int8(x) for x in w1], [O.act_int8(x) for x in w2]
+
+
+def _check_moe(out, ref, mag, topk):
+    err = np.abs(out.astype(np.float64) - ref)
+    assert (err <= (topk + 5) * U * mag + 1e-38).all()
+
+
+MOE = [(1, 4, 1, 64, 32), (1, 8, 6, 96, 160), (5, 3, 2, 32, 64), (12, 8, 2, 96, 64),
+       (16, 16, 6, 352, 416), (40, 4, 3, 160, 96), (150, 4, 2, 64, 288), (130, 2, 1, 192, 320),
+       (600, 3, 2, 96, 64)]
+
+
+@pytest.mark.parametrize("t,e,topk,n1,k", MOE)
+def test_moe_equals_oracle(dev, t, e, topk, n1, k):
+    c1, c2, w1, w2 = _experts(dev, e, n1, k, seed=t)
+    x = _acts(t, k, seed=t + 1)
+    ids, g = I.route(np.random.default_rng(t).standard_normal((t, e)), topk)
+    out = _ops().moe_grouped_int8(_bf16(x, dev), torch.from_numpy(ids).to(dev),
+                                  torch.from_numpy(g).to(dev), c1, c2, e, n1)
+    ref, mag = O.moe_int8(x, ids, g, w1, w2)
+    _check_moe(out.cpu().numpy(), ref, mag, topk)
+
+
+def test_moe_skipped_slots_repeated_ids_and_padded_rows(dev):
+    t, e, topk, n1, k = 40, 4, 3, 96, 128
+    c1, c2, w1, w2 = _experts(dev, e, n1, k, seed=9)
+    x = _acts(t, k, seed=10)
+    rng = np.random.default_rng(11)
+    ids = rng.integers(-2, e + 2, (t, topk)).astype(np.int32)   # some outside, some repeated
+    ids[5] = 2                                                  # one expert in every slot
+    ids[30:] = -1                                               # rows that fill up the batch
+    g = rng.random((t, topk)).astype(np.float32)
+    out = _ops().moe_grouped_int8(_bf16(x, dev), torch.from_numpy(ids).to(dev),
+                                  torch.from_numpy(g).to(dev), c1, c2, e, n1).cpu().numpy()
+    ref, mag = O.moe_int8(x, ids, g, w1, w2)
+    _check_moe(out, ref, mag, topk)
+    assert (out[30:] == 0).all()
+
+
+@pytest.mark.parametrize("t", [3, 200])
+def test_moe_all_tokens_on_one_expert_or_none(dev, t):
+    e, topk, n1, k = 6, 2, 64, 96
+    c1, c2, w1, w2 = _experts(dev, e, n1, k, seed=2)
+    x = _acts(t, k, seed=3)
+    g = np.full((t, topk), 0.25, np.float32)
+    ids = np.tile(np.array([5, 0], np.int32), (t, 1))
+    out = _ops().moe_grouped_int8(_bf16(x, dev), torch.from_numpy(ids).to(dev),
+                                  torch.from_numpy(g).to(dev), c1, c2, e, n1).cpu().numpy()
+    ref, mag = O.moe_int8(x, ids, g, w1, w2)
+    _check_moe(out, ref, mag, topk)
+    out = _ops().moe_grouped_int8(_bf16(x, dev), torch.full((t, topk), -1, dtype=torch.int32,
+                                                            device=dev),
+                                  torch.from_numpy(g).to(dev), c1, c2, e, n1)
+    assert (out == 0).all()
+
+
+def test_moe_nan_stays_in_its_tokens(dev):
+    t, e, topk, n1, k = 20, 4, 2, 64, 96
+    c1, c2, _, _ = _experts(dev, e, n1, k, seed=7)
+    x = _acts(t, k, seed=8)
+    x[3, 4] = 0x7F80
+    ids, g = I.route(np.random.default_rng(1).standard_normal((t, e)), topk)
+    out = _ops().moe_grouped_int8(_bf16(x, dev), torch.from_numpy(ids).to(dev),
+                                  torch.from_numpy(g).to(dev), c1, c2, e, n1).cpu().numpy()
+    assert np.isnan(out[3]).all() and np.isfinite(np.delete(out, 3, 0)).all()
+
+
+def test_moe_full_size_layer_is_its_parts(dev):
+    """128 experts of the model's sizes: tokens one at a time, in a batch of 16 and
+    in a batch of 700 give the same bits, and a few tokens equal the oracle."""
+    wl = I.WORKLOADS["moe_t16"]
+    e, n1, k, topk, t = wl.n_experts, wl.n1, wl.k, wl.topk, 700
+    gen = torch.Generator(device=dev).manual_seed(5)
+    w1 = (0.02 * torch.randn(e * n1, k, generator=gen, device=dev)).to(torch.bfloat16)
+    w2 = (0.02 * torch.randn(e * k, n1, generator=gen, device=dev)).to(torch.bfloat16)
+    c1, c2 = _ops().int8_cache_bf16(w1), _ops().int8_cache_bf16(w2)
+    x = _acts(t, k, seed=6)
+    ids, g = I.route(I.router_logits(t, e, "zipf"), topk)
+    xg, ig, gg = _bf16(x, dev), torch.from_numpy(ids).to(dev), torch.from_numpy(g).to(dev)
+    out = _ops().moe_grouped_int8(xg, ig, gg, c1, c2, e, n1)
+    part = _ops().moe_grouped_int8(xg[:16].contiguous(), ig[:16].contiguous(),
+                                   gg[:16].contiguous(), c1, c2, e, n1)
+    assert torch.equal(part, out[:16])
+    one = _ops().moe_grouped_int8(xg[9:10].contiguous(), ig[9:10].contiguous(),
+                                  gg[9:10].contiguous(), c1, c2, e, n1)
+    assert torch.equal(one, out[9:10])
+    some = [0, 9, 699]
+    v1, v2 = _ops().int8_cache_views(c1, e * n1, k), _ops().int8_cache_views(c2, e * k, n1)
+    need = sorted(set(ids[some].ravel().tolist()))
+    l1 = {i: tuple(v[i * n1:(i + 1) * n1].cpu().numpy() for v in v1) for i in need}
+    l2 = {i: tuple(v[i * k:(i + 1) * k].cpu().numpy() for v in v2) for i in need}
+    l1 = {i: (c[:, :k], s) for i, (c, s) in l1.items()}
+    l2 = {i: (c[:, :n1], s) for i, (c, s) in l2.items()}
+    lists = [[d.get(i) for i in range(e)] for d in (l1, l2)]
+    ref, mag = O.moe_int8(x[some], ids[some], g[some], *lists)
+    _check_moe(out[some].cpu().numpy(), ref, mag, topk)
+
+
+# ---- the scored router -----------------------------------------------------
+
+def _check_router(dev, lg, topk, **kw):
+    bias = kw.get("bias")
+    ids, w = _ops().moe_router_scored(
+        torch.from_numpy(lg).to(dev), topk,
+        **dict(kw, bias=None if bias is None else torch.from_numpy(bias).to(dev)))
+    ri, rw = O.router_scored(lg, topk, **kw)
+    assert np.array_equal(ids.cpu().numpy(), ri)
+    err = np.abs(w.cpu().numpy().astype(np.float64) - rw)
+    assert (err <= 1.001 * U * np.abs(rw) + 2.0 ** -149).all()
+    return ids, w
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("t,e,topk,groups,keep", [
+    (1, 1, 1, 1, 1), (3, 2, 2, 1, 1), (16, 128, 6, 1, 1), (5, 65, 64, 1, 1), (4, 512, 512, 1, 1),
+    (7, 512, 70, 1, 1), (9, 64, 8, 8, 3), (11, 160, 6, 8, 3), (6, 256, 8, 8, 4), (5, 12, 3, 12, 3),
+    (4, 512, 8, 512, 9), (33, 40, 5, 2, 1), (8, 96, 8, 4, 4), (300, 128, 6, 1, 1),
+    (130, 256, 8, 8, 4)])
+def test_router_equals_oracle(dev, score, t, e, topk, groups, keep):
+    rng = np.random.default_rng(t * e)
+    lg = (2.0 * rng.standard_normal((t, e))).astype(np.float32)
+    bias = (0.2 * rng.standard_normal(e)).astype(np.float32)
+    for b, renorm, scale in ((None, False, 1.0), (bias, True, 2.5), (bias, False, 0.5),
+                             (None, True, 1.0)):
+        _check_router(dev, lg, topk, score=score, bias=b, n_groups=groups, topk_groups=keep,
+                      renormalize=renorm, scale=scale)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (4, 2), (8, 5)])
+def test_router_switched_off_experts(dev, score, groups, keep):
+    """Rows with every share of experts off, from none to all; NaN; both infinities;
+    the type's lowest and highest value; an infinite and a NaN bias."""
+    e, topk = 40, 6 if groups < 8 else 5
+    rng = np.random.default_rng(5)
+    lg = rng.standard_normal((48, e)).astype(np.float32)
+    for i in range(41):
+        lg[i, rng.permutation(e)[:i]] = -np.inf
+    lg[41, 3] = np.nan
+    lg[42, :] = np.nan
+    lg[43, 7] = np.inf
+    lg[44, :] = np.finfo(np.float32).min
+    lg[45, ::2] = np.finfo(np.float32).min
+    lg[46, 5] = np.finfo(np.float32).max
+    lg[47, :] = np.float32(-200.0)
+    for bias in (None, (0.3 * rng.standard_normal(e)).astype(np.float32)):
+        for renorm in (False, True):
+            _check_router(dev, lg, topk, score=score, bias=bias, n_groups=groups,
+                          topk_groups=keep, renormalize=renorm, scale=1.5)
+    bias[4], bias[9], bias[20] = -np.inf, np.nan, np.inf
+    _check_router(dev, lg, topk, score=score, bias=bias, n_groups=groups, topk_groups=keep,
+                  renormalize=True)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (8, 3)])
+def test_router_ties_and_near_ties(dev, score, groups, keep):
+    """Logits of few distinct values (ties go to the lower id) and logits one fp32
+    step apart, where only more than 32 bits tell the scores apart."""
+    e = 64
+    rng = np.random.default_rng(8)
+    few = rng.integers(-2, 3, (64, e)).astype(np.float32) * np.float32(0.5)
+    base = rng.standard_normal((64, 1)).astype(np.float32)
+    near = (base.view(np.int32) + rng.integers(0, 6, (64, e)).astype(np.int32)).view(np.float32)
+    equal = np.zeros((4, e), np.float32)
+    for lg in (few, near, equal):
+        for bias in (None, np.repeat(np.float32([0.0, 0.25]), e // 2)):
+            _check_router(dev, lg, 8, score=score, bias=bias, n_groups=groups, topk_groups=keep,
+                          renormalize=True)
+
+
+def test_router_agrees_with_the_softmax_router(dev):
+    lg = torch.randn(500, 128, device=dev)
+    ids, g = _ops().moe_router(lg, 6)
+    ids2, g2 = _ops().moe_router_scored(lg, 6)
+    assert torch.equal(ids, ids2)
+    assert torch.allclose(g, g2, rtol=1e-5, atol=0)
+
+
+def test_router_refusals(dev):
+    from block_diffusion_lm_tq4_amd._lib import TQ4Error
+    lg = torch.zeros(4, 12, device=dev)
+    with pytest.raises(ValueError, match="score"):
+        _ops().moe_router_scored(lg, 2, score="tanh")
+    with pytest.raises(ValueError, match="bias"):
+        _ops().moe_router_scored(lg, 2, bias=torch.zeros(11, device=dev))
+    with pytest.raises(TQ4Error, match="SHAPE"):
+        _ops().moe_router_scored(lg, 2, n_groups=5)
+    with pytest.raises(TQ4Error, match="SHAPE"):
+        _ops().moe_router_scored(lg, 5, n_groups=3, topk_groups=1)
+    ids, w = _ops().moe_router_scored(torch.zeros(0, 12, device=dev), 2)
+    assert ids.shape == (0, 2) and w.shape == (0, 2)
+
+
+# ---- together --------------------------------------------------------------
+
+def _layer(dev, seed=0):
+    """A dense projection with residual, the router and the MoE layer after it."""
+    m, k, n1, e, topk = 24, 128, 96, 8, 2
+    gen = torch.Generator(device=dev).manual_seed(seed)
+    w = (0.1 * torch.randn(k, k, generator=gen, device=dev)).to(torch.bfloat16)
+    wr = (0.1 * torch.randn(e, k, generator=gen, device=dev)).to(torch.bfloat16)
+    w1 = (0.1 * torch.randn(e * n1, k, generator=gen, device=dev)).to(torch.bfloat16)
+    w2 = (0.1 * torch.randn(e * k, n1, generator=gen, device=dev)).to(torch.bfloat16)
+    o = _ops()
+    c, cr, c1, c2 = (o.int8_cache_bf16(v) for v in (w, wr, w1, w2))
+    bias = 0.1 * torch.randn(e, generator=gen, device=dev)
+    x = torch.randn(m, k, generator=gen, device=dev).to(torch.bfloat16)
+
+    def run():
+        h = o.linear_int8_epilogue_bf16(x, c, k, None, x)
+        q, s = o.act_int8(h)
+        logits = o.linear_int8_quantized(q, s, k, cr, e)
+        ids, g = o.moe_router_scored(logits, topk, score="sigmoid", bias=bias, n_groups=4,
+                                     topk_groups=2, renormalize=True, scale=2.5)
+        return h, logits, ids, g, o.moe_grouped_int8(h, ids, g, c1, c2, e, n1)
+
+    return x, run, (c1, c2, e, n1, k)
+
+
+def test_layer_together(dev):
+    x, run, (c1, c2, e, n1, k) = _layer(dev)
+    h, logits, ids, g, out = run()
+    bits = h.view(torch.int16).cpu().numpy().view(np.uint16)
+    v1 = [v.cpu().numpy() for v in _ops().int8_cache_views(c1, e * n1, k)]
+    v2 = [v.cpu().numpy() for v in _ops().int8_cache_views(c2, e * k, n1)]
+    l1 = [(v1[0][i * n1:(i + 1) * n1, :k], v1[1][i * n1:(i + 1) * n1]) for i in range(e)]
+    l2 = [(v2[0][i * k:(i + 1) * k, :n1], v2[1][i * k:(i + 1) * k]) for i in range(e)]
+    ref, mag = O.moe_int8(bits, ids.cpu().numpy(), g.cpu().numpy(), l1, l2)
+    _check_moe(out.cpu().numpy(), ref, mag, 2)
+
+
+def test_layer_in_a_graph(dev):
+    """Captured once, replayed with new inputs, eager calls in between."""
+    x, run, _ = _layer(dev, seed=1)
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for i in range(4):
+        x.copy_(torch.randn_like(x.float(), dtype=torch.float32).to(torch.bfloat16))
+        eager = [v.clone() for v in run()]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, eager))
+
+
+def test_two_streams_and_two_graphs_do_not_share_scratch(dev):
+    runs = [_layer(dev, seed=s)[1] for s in (2, 3)]
+    refs = [[v.clone() for v in r()] for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(runs[i]())
+    torch.cuda.synchronize()
+    for i in range(2):
+        for res in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(res, refs[i]))
+    graphs, held = [], []
+    for r in runs:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            held.append(r())
+        graphs.append(gr)
+    for _ in range(5):
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(held[i], refs[i]))
+
+
+def test_repeated_calls_give_the_same_bits(dev):
+    calls = []
+    for m, k, n in ((1, 2688, 2000), (16, 2688, 8192), (40, 1856, 900), (333, 1856, 2688),
+                    (700, 2688, 1500)):
+        cache, _, _ = _weights(dev, n, k, seed=m)
+        x = _bf16(_acts(m, k, seed=m), dev)
+        calls.append(lambda x=x, c=cache, n=n: _ops().linear_int8(x, c, n))
+    first = [f().clone() for f in calls]
+    bad = sum(not torch.equal(f(), r) for _ in range(30) for f, r in zip(calls, first))
+    assert bad == 0
