@@ -867,13 +867,13 @@ int tq4_moe_grouped_int8(const uint16_t *x_bf16, int64_t t, int64_t k, const int
     e = tq4::launch_route(topk_ids, pairs, topk, n_experts, counts, offsets, perm, inv, tiles,
                           meta, l.tile_rows, nullptr, s);
   if (e == hipSuccess)
-    e = tq4::launch_moe_int8(0, l.tile_rows, xq, xs, k, perm, topk,
+    e = tq4::launch_moe_int8(0, l.tile_rows, xq, xs, t, k, perm, topk,
                              reinterpret_cast<const int8_t *>(w1_cache),
                              int8_scales(w1_cache, e64 * n1, k), n1, tiles, meta, l.max_tiles, h,
                              s);
   if (e == hipSuccess) e = tq4::launch_act_int8(h, pairs, n1, hq, hs, s);
   if (e == hipSuccess)
-    e = tq4::launch_moe_int8(1, l.tile_rows, hq, hs, n1, perm, topk,
+    e = tq4::launch_moe_int8(1, l.tile_rows, hq, hs, pairs, n1, perm, topk,
                              reinterpret_cast<const int8_t *>(w2_cache),
                              int8_scales(w2_cache, e64 * k, n1), k, tiles, meta, l.max_tiles, o,
                              s);

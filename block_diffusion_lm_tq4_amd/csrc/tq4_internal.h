@@ -339,13 +339,13 @@ hipError_t launch_linear_int8(const int8_t *xq, const float *xs, int64_t m, int6
                               void *y, hipStream_t s);
 // Grouped products over stacked int8 experts (expert e's rows at e * n of the
 // [E * n, k] cache).  mode 0 (up): rows gathered as perm[row] / topk; out is
-// bf16 [pairs][n], relu(u)^2.  mode 1 (down): bucket rows; out is fp32
+// bf16 [pairs][n], relu(u)^2.  a_rows: rows of aq.  mode 1 (down): bucket rows; out is fp32
 // [pairs][n].  tile_rows as int8_moe_tile_rows gives (and launch_route got).
 int int8_moe_tile_rows(int64_t pairs, int32_t n_experts);
-hipError_t launch_moe_int8(int mode, int tile_rows, const int8_t *aq, const float *as, int64_t k,
-                           const int32_t *perm, int32_t topk, const int8_t *wq, const float *ws,
-                           int64_t n, const MoETile *tiles, const int32_t *n_tiles,
-                           int64_t max_tiles, void *out, hipStream_t s);
+hipError_t launch_moe_int8(int mode, int tile_rows, const int8_t *aq, const float *as,
+                           int64_t a_rows, int64_t k, const int32_t *perm, int32_t topk,
+                           const int8_t *wq, const float *ws, int64_t n, const MoETile *tiles,
+                           const int32_t *n_tiles, int64_t max_tiles, void *out, hipStream_t s);
 
 // Streaming read of `bytes` (a multiple of 16) from a 16-byte aligned buffer.
 hipError_t launch_read_probe(const void *src, int64_t bytes, float *sink, hipStream_t s);
