@@ -282,18 +282,32 @@ __device__ inline float hidden_f64(int acc, float sx, float sw) {
   return static_cast<float>(h);
 }
 
-// The same in fp32 where that decides it: u carries at most three roundings
-// and its square seven, 7 * 2^-24 relative, i.e. at most 7 fp32 steps, so the
-// bf16 rounding is settled unless the low 16 bits are within 8 of the tie;
-// about one value in 4000 takes fp64.
-__device__ inline uint16_t hidden_of(int acc, float sx, float sw) {
-  const float u = (static_cast<float>(acc) * sx) * sw;
-  float h = acc > 0 ? u * u : 0.f;
-  const uint32_t low = (__float_as_uint(h) & 0xFFFFu) - (0x8000u - 8u);
-  const bool plain = h >= 0x1p-100f && h <= 0x1p+100f && low > 16u;
-  // 0 * inf can only come from scales whose product overflows: fp64 tells
-  if (!plain && (acc > 0 || __builtin_isnan(u))) h = hidden_f64(acc, sx, sw);
-  return bf16_bits(h);
+// The same for four sums of one row, in fp32 where that decides it.  With both
+// scales zero or in [2^-30, 2^16] (`tame`) nothing leaves fp32's normal range:
+// u = acc * (sx * sw) carries at most three roundings and its square seven, 7 *
+// 2^-24 relative, i.e. at most 7 fp32 steps, so the bf16 rounding is settled
+// unless the low 16 bits are within 8 of the tie.  About one value in 4000 is
+// not, and its quad takes fp64.  (Written with a test for each value, this was
+// 100 of the up product's 250 us at 4096 tokens.)
+__device__ inline bool tame_scale(float s) {
+  return s == 0.f || (s >= 0x1p-30f && s <= 0x1p+16f);
+}
+
+__device__ inline uint2 hidden_quad(intx4 acc, float sx, const float (&sw)[4], bool tame) {
+  float h[4];
+  bool slow = !tame;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const float u = static_cast<float>(acc[v] > 0 ? acc[v] : 0) * (sx * sw[v]);
+    h[v] = u * u;
+    slow |= ((__float_as_uint(h[v]) - (0x8000u - 8u)) & 0xFFFFu) <= 16u;
+  }
+  if (__builtin_expect(__any(slow), 0)) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) h[v] = hidden_f64(acc[v], sx, sw[v]);
+  }
+  return make_uint2(bf16_bits(h[0]) | static_cast<uint32_t>(bf16_bits(h[1])) << 16,
+                    bf16_bits(h[2]) | static_cast<uint32_t>(bf16_bits(h[3])) << 16);
 }
 
 // One row's four consecutive outputs n .. n + 3 of the MoE products (n % 32
@@ -303,13 +317,10 @@ __device__ inline void store_moe(const I8Args &g, intx4 acc, int64_t row, int64_
                                  const float (&sw)[4]) {
   if (n >= g.n) return;
   if constexpr (MODE == kI8Up) {
-    uint32_t w[2];
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-      w[v] = static_cast<uint32_t>(hidden_of(acc[2 * v], sx, sw[2 * v])) |
-             static_cast<uint32_t>(hidden_of(acc[2 * v + 1], sx, sw[2 * v + 1])) << 16;
+    const bool tame = tame_scale(sx) && tame_scale(sw[0]) && tame_scale(sw[1]) &&
+                      tame_scale(sw[2]) && tame_scale(sw[3]);
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.y) + row * g.n + n) =
-        make_uint2(w[0], w[1]);
+        hidden_quad(acc, sx, sw, tame);
   } else {
     float p[4];
 #pragma unroll
@@ -546,6 +557,172 @@ __global__ __launch_bounds__(64 * KW) void i8_skinny_kernel(I8Args g) {
   }
 }
 
+// A wave's MS x NS sub-tiles to memory through LDS.  Straight from the product's
+// layout a store instruction would write 16 rows x 64 bytes (32 for bf16),
+// half a cache line each; instead 16 rows at a time go to a wave's own LDS
+// buffer (two in turn, rows 16 bytes longer than their data, so that neither
+// the writes nor the reads share banks) and come back as whole row segments
+// of 16 * NS outputs.  Stores are non-temporal in the dense mode, whose
+// output is larger than the caches it would push the operands out of.
+// Residual values of the next 16 rows are loaded before the stores of these,
+// since a wait for a load is also one for every store before it.
+template <int NS>
+constexpr int tile_store_bytes() {
+  return 2 * 16 * (16 * NS + 4) * 4;
+}
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t uintx2 __attribute__((ext_vector_type(2)));
+
+template <int MODE, int MS, int NS, int WM, bool BF16, bool VEC>
+__device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], uint8_t *lds,
+                                  int64_t m0, int rows, int64_t n0, int64_t w0,
+                                  const float (&sx)[MS], int lane) {
+#pragma clang fp contract(off)
+  constexpr int kCols = 16 * NS;
+  constexpr int kStride = kCols + 4;
+  constexpr int E = VEC ? 4 : 1;             // outputs per lane and access
+  constexpr int kGroups = 16 * kCols / (64 * E);
+  const int r = lane % 16;
+  const int grp = lane / 16;
+  const bool has_bias = MODE == kI8Dense && g.tail.bias != nullptr;
+  const bool has_res = MODE == kI8Dense && g.tail.residual != nullptr;
+  float sw[NS][4];
+#pragma unroll
+  for (int j = 0; j < NS; ++j)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t n = n0 + 16 * j + 4 * grp + v;
+      sw[j][v] = n < g.n ? g.ws[w0 + n] : 0.f;
+    }
+  // this lane's columns in the row image are the same for every group of rows
+  // when a row is a divisor of 64 * E outputs, which it is for NS = 1, 2, 4
+  // (and 8 with E = 4 loops twice over half-waves' rows)
+  float res[kGroups][E];
+  auto load_res = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      const int f = 64 * E * q + E * lane;
+      const int row = 16 * WM * i + f / kCols;
+      const int64_t n = n0 + f % kCols;
+#pragma unroll
+      for (int v = 0; v < E; ++v) res[q][v] = 0.f;
+      if (row < rows && n < g.n) {
+        const int64_t at = (m0 + row) * g.n + n;
+        if constexpr (VEC && BF16) {
+          const uintx2 d =
+              *reinterpret_cast<const uintx2 *>(static_cast<const uint16_t *>(g.tail.residual) + at);
+          res[q][0] = __uint_as_float(d.x << 16);
+          res[q][1] = __uint_as_float(d.x & 0xFFFF0000u);
+          res[q][2] = __uint_as_float(d.y << 16);
+          res[q][3] = __uint_as_float(d.y & 0xFFFF0000u);
+        } else if constexpr (VEC) {
+          const floatx4 d =
+              *reinterpret_cast<const floatx4 *>(static_cast<const float *>(g.tail.residual) + at);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) res[q][v] = d[v];
+        } else {
+          res[q][0] = tail_residual_as<BF16>(g.tail.residual, at);
+        }
+      }
+    }
+  };
+  if (has_res) load_res(0);
+  if constexpr (MODE == kI8Up) {
+    // the row image is bf16: 2 * kStride bytes per row, eight outputs per lane
+    bool tame = true;
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) tame = tame && tame_scale(sw[j][v]);
+#pragma unroll
+    for (int i = 0; i < MS; ++i) tame = tame && tame_scale(sx[i]);
+    constexpr int kRowBytes = 2 * kCols + 16;
+    constexpr int kReads = 16 * kCols / 512;  // of 64 lanes x 8 outputs
+    static_assert(kReads >= 1, "two or more column sub-tiles");
+#pragma unroll
+    for (int i = 0; i < MS; ++i) {
+      if (16 * WM * i >= rows) break;
+      uint8_t *buf = lds + (i % 2) * (16 * kRowBytes);
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+        *reinterpret_cast<uint2 *>(buf + r * kRowBytes + 32 * j + 8 * grp) =
+            hidden_quad(acc[i][j], sx[i], sw[j], tame);
+#pragma unroll
+      for (int q = 0; q < kReads; ++q) {
+        const int f = 512 * q + 8 * lane;
+        const uint4 d = *reinterpret_cast<const uint4 *>(buf + (f / kCols) * kRowBytes +
+                                                         2 * (f % kCols));
+        const int row = 16 * WM * i + f / kCols;
+        const int64_t n = n0 + f % kCols;
+        if (row < rows && n < g.n)  // n % 32 == 0 columns in all
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(g.y) + (m0 + row) * g.n + n) = d;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < MS; ++i) {
+    if (MODE != kI8Dense && 16 * WM * i >= rows) break;
+    float *buf = reinterpret_cast<float *>(lds) + (i % 2) * (16 * kStride);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      floatx4 p;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) p[v] = (static_cast<float>(acc[i][j][v]) * sx[i]) * sw[j][v];
+      *reinterpret_cast<floatx4 *>(buf + r * kStride + 16 * j + 4 * grp) = p;
+    }
+    float val[kGroups][E];
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      const int f = 64 * E * q + E * lane;
+      const float *src = buf + (f / kCols) * kStride + f % kCols;
+      if constexpr (VEC) {
+        const floatx4 d = *reinterpret_cast<const floatx4 *>(src);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) val[q][v] = d[v];
+      } else {
+        val[q][0] = *src;
+      }
+      if constexpr (MODE == kI8Dense) {
+        const int64_t n = n0 + f % kCols;
+#pragma unroll
+        for (int v = 0; v < E; ++v) {
+          if (has_bias) val[q][v] += n < g.n ? g.tail.bias[n + v] : 0.f;
+          if (has_res) val[q][v] += res[q][v];
+        }
+      }
+    }
+    if (has_res && i + 1 < MS) load_res(i + 1);
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      const int f = 64 * E * q + E * lane;
+      const int row = 16 * WM * i + f / kCols;
+      const int64_t n = n0 + f % kCols;
+      if (row >= rows || n >= g.n) continue;
+      const int64_t at = (m0 + row) * g.n + n;
+      if constexpr (VEC && BF16) {
+        const uintx2 d = {bf16_bits(val[q][0]) | static_cast<uint32_t>(bf16_bits(val[q][1])) << 16,
+                          bf16_bits(val[q][2]) | static_cast<uint32_t>(bf16_bits(val[q][3])) << 16};
+        uintx2 *dst = reinterpret_cast<uintx2 *>(static_cast<uint16_t *>(g.y) + at);
+        if constexpr (MODE != kI8Up)
+          __builtin_nontemporal_store(d, dst);
+        else
+          *dst = d;
+      } else if constexpr (VEC) {
+        const floatx4 d = {val[q][0], val[q][1], val[q][2], val[q][3]};
+        floatx4 *dst = reinterpret_cast<floatx4 *>(static_cast<float *>(g.y) + at);
+        if constexpr (MODE != kI8Up)
+          __builtin_nontemporal_store(d, dst);
+        else
+          *dst = d;
+      } else {
+        tail_store_as<BF16>(static_cast<float *>(g.y), at, val[q][0]);
+      }
+    }
+  }
+}
+
 // ---- many rows --------------------------------------------------------------
 // TM x TN output tile per workgroup of WM x WN waves, each wave MS x NS
 // 16 x 16 products.  KB bytes (64 or 128) of k of the tile's TM activation
@@ -558,7 +735,7 @@ __global__ __launch_bounds__(64 * KW) void i8_skinny_kernel(I8Args g) {
 // at one slot fall on all 64 banks.  Rows past the tile's end read zeros
 // (dense; the buffer range ends there) or the tile's first row (MoE) and are
 // not stored.
-template <int MODE, int WM, int WN, int MS, int NS, int KB, int S, int OCC>
+template <int MODE, int WM, int WN, int MS, int NS, int KB, int S, int OCC, bool PP>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
   constexpr int W = WM * WN;
   constexpr int TM = 16 * MS * WM;
@@ -588,7 +765,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
   int rows;  // valid rows of the tile
   if constexpr (MODE == kI8Dense) {
     // Workgroup ids go round robin over the 8 XCDs.  Each XCD takes one
-    // contiguous run of an order that walks blocks of 4 tile columns down
+    // contiguous run of an order that walks blocks of 8 tile columns down
     // all tile rows, so the tiles it holds at a time share their operands in
     // its L2.
     const int total = g.tiles_m * g.tiles_n;
@@ -596,20 +773,20 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
     const int x = id % 8;
     const int q = total / 8, rem = total % 8;
     const int at = x * q + (x < rem ? x : rem) + id / 8;
-    const int blk = at / (4 * g.tiles_m);
-    const int in = at % (4 * g.tiles_m);
-    const int width = g.tiles_n - 4 * blk < 4 ? g.tiles_n - 4 * blk : 4;
+    const int blk = at / (8 * g.tiles_m);
+    const int in = at % (8 * g.tiles_m);
+    const int width = g.tiles_n - 8 * blk < 8 ? g.tiles_n - 8 * blk : 8;
     m_base = static_cast<int64_t>(in / width) * TM;
-    n_base = static_cast<int64_t>(4 * blk + in % width) * TN;
+    n_base = static_cast<int64_t>(8 * blk + in % width) * TN;
     rows = g.m - m_base < TM ? static_cast<int>(g.m - m_base) : TM;
   } else {
-    const int per = (g.tiles_n + 7) / 8;
+    // XCD x (workgroup id % 8) takes tiles x, x + 8, ... with all their column
+    // blocks in a row: the tile's rows then stay in one L2
     const int q = static_cast<int>(blockIdx.x) / 8;
-    const int i = q / per;
+    const int i = q / g.tiles_n * 8 + static_cast<int>(blockIdx.x) % 8;
     if (i >= *g.n_tiles) return;
     const MoETile t = g.tiles[i];
-    const int j = (static_cast<int>(blockIdx.x) + t.expert) % 8 + 8 * (q % per);
-    if (j >= g.tiles_n) return;
+    const int j = q % g.tiles_n;
     m_base = t.row0;
     rows = t.rows;
     n_base = static_cast<int64_t>(j) * TN;
@@ -675,9 +852,12 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
 
   // fragment addresses: row 16 * x + r, whose key depends on r alone
   const int key = KB == 64 ? (r >> 2) & 3 : (r >> 1) & 7;
-  const int a_frag = (wm * (16 * MS) + r) * KB;
+  const int a_frag = (16 * wm + r) * KB;
   const int w_frag = kWBase + (wn * (16 * NS) + r) * KB;
-  const bool idle = MODE != kI8Dense && wm * (16 * MS) >= rows;
+  // A wave's sub-tile i holds rows 16 (WM i + wm) ..., so that the rows of a
+  // part-filled tile are spread over the waves; sub-tiles past the rows are
+  // skipped, two at a time.
+  const int live = MODE == kI8Dense ? MS : (rows - 16 * wm + 16 * WM - 1) / (16 * WM);
   auto half = [&](const uint8_t *st, int h) __attribute__((always_inline)) {
     const int slot = 16 * ((4 * h + grp) ^ key);
     intx4 wf[NS];
@@ -686,7 +866,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
       wf[j] = *reinterpret_cast<const intx4 *>(st + w_frag + 16 * j * KB + slot);
 #pragma unroll
     for (int i = 0; i < MS; ++i) {
-      const intx4 af = *reinterpret_cast<const intx4 *>(st + a_frag + 16 * i * KB + slot);
+      if (MODE != kI8Dense && i % 2 == 0 && i >= live) break;
+      const intx4 af = *reinterpret_cast<const intx4 *>(st + a_frag + 16 * WM * i * KB + slot);
 #pragma unroll
       for (int j = 0; j < NS; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[j], af, acc[i][j], 0, 0, 0);
@@ -698,51 +879,96 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
   static_assert(kAhead < 64, "the wait counts up to 63 loads");
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) issue(s, smem + s * kStage);
-  for (int c = 0; c < steps; c += S) {
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      // step c + s has landed when only the S - 2 steps after it are in
-      // flight; behind the barrier it has for every wave, and every wave has
-      // read step c + s - 1, whose stage is then refilled
-      __builtin_amdgcn_s_waitcnt(kWait);
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  if constexpr (PP) {
+    static_assert(W == 8 && KB == 64, "two waves per SIMD, one product step per stage");
+    const bool late = wave >= 4;
+    intx4 wf[NS], af[MS];
+    const int slot = 16 * (grp ^ key);
+    auto phase_end = [&]() __attribute__((always_inline)) {
+      __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_barrier();
-      issue(c + s + S - 1, smem + ((s + S - 1) % S) * kStage);
-      if (c + s < steps && !idle) {
-        half(smem + s * kStage, 0);
-        if (KB == 128 && 2 * (c + s) + 1 < halves) half(smem + s * kStage, 1);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    __builtin_amdgcn_s_waitcnt(kWait);  // step 0
+    phase_end();
+    if (late) phase_end();
+    for (int c = 0; c < steps; c += S) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        if (c + s < steps) {
+          const uint8_t *st = smem + s * kStage;
+#pragma unroll
+          for (int j = 0; j < NS; ++j)
+            wf[j] = *reinterpret_cast<const intx4 *>(st + w_frag + 16 * j * KB + slot);
+#pragma unroll
+          for (int i = 0; i < MS; ++i)
+            af[i] = *reinterpret_cast<const intx4 *>(st + a_frag + 16 * WM * i * KB + slot);
+          issue(c + s + S - 1, smem + ((s + S - 1) % S) * kStage);
+          __builtin_amdgcn_s_waitcnt(kWait);   // step c + s + 1
+          __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+          phase_end();
+#pragma unroll
+          for (int i = 0; i < MS; ++i) {
+            if (MODE != kI8Dense && i % 2 == 0 && i >= live) break;
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[j], af[i], acc[i][j], 0, 0, 0);
+          }
+          phase_end();
+        }
+      }
+    }
+    if (!late) phase_end();
+  } else {
+    for (int c = 0; c < steps; c += S) {
+  #pragma unroll
+      for (int s = 0; s < S; ++s) {
+        // step c + s has landed when only the S - 2 steps after it are in
+        // flight; behind the barrier it has for every wave, and every wave has
+        // read step c + s - 1, whose stage is then refilled
+        __builtin_amdgcn_s_waitcnt(kWait);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        issue(c + s + S - 1, smem + ((s + S - 1) % S) * kStage);
+        if (c + s < steps) {
+          half(smem + s * kStage, 0);
+          if (KB == 128 && 2 * (c + s) + 1 < halves) half(smem + s * kStage, 1);
+        }
       }
     }
   }
+  static_assert(W * tile_store_bytes<NS>() <= S * kStage, "the stages hold the store buffers");
   __builtin_amdgcn_s_waitcnt(0x0F70);  // the padding steps' loads
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // the last reads of the stages
+  __syncthreads();                     // for every wave: the stages become store buffers
 
-  if (idle) return;
   float sx[MS];
 #pragma unroll
   for (int i = 0; i < MS; ++i) {
-    const int row = wm * (16 * MS) + 16 * i + r;
+    const int row = 16 * (WM * i + wm) + r;
     const int64_t b = m_base + (row < rows ? row : 0);
     sx[i] = g.xs[MODE == kI8Up ? g.perm[b] / g.topk : b];
   }
-  if constexpr (MODE == kI8Dense) {
-    store_any<MS, NS>(g, acc, m_base + wm * (16 * MS), rows - wm * (16 * MS),
-                      n_base + wn * (16 * NS), sx, lane);
+  uint8_t *lds = smem + wave * tile_store_bytes<NS>();
+  const int64_t m0 = m_base + 16 * wm;
+  const int64_t n0 = n_base + wn * (16 * NS);
+  rows -= 16 * wm;
+  if constexpr (MODE != kI8Dense) {
+    store_rows<MODE, MS, NS, WM, MODE == kI8Up, true>(g, acc, lds, m0, rows, n0, w0, sx, lane);
+  } else if (g.vec) {
+    if (g.tail.bf16)
+      store_rows<MODE, MS, NS, WM, true, true>(g, acc, lds, m0, rows, n0, 0, sx, lane);
+    else
+      store_rows<MODE, MS, NS, WM, false, true>(g, acc, lds, m0, rows, n0, 0, sx, lane);
   } else {
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      const int64_t n = n_base + wn * (16 * NS) + 16 * j + 4 * grp;
-      float sw[4];
-      load_sw(g, w0, n, sw);
-#pragma unroll
-      for (int i = 0; i < MS; ++i) {
-        const int row = wm * (16 * MS) + 16 * i + r;
-        if (row < rows) store_moe<MODE>(g, acc[i][j], m_base + row, n, sx[i], sw);
-      }
-    }
+    if (g.tail.bf16)
+      store_rows<MODE, MS, NS, WM, true, false>(g, acc, lds, m0, rows, n0, 0, sx, lane);
+    else
+      store_rows<MODE, MS, NS, WM, false, false>(g, acc, lds, m0, rows, n0, 0, sx, lane);
   }
 }
 
-template <int MODE, int WM, int WN, int MS, int NS, int KB, int S, int OCC>
+template <int MODE, int WM, int WN, int MS, int NS, int KB, int S, int OCC, bool PP = false>
 hipError_t launch_tile(I8Args g, int64_t max_tiles, hipStream_t s) {
   constexpr int TM = 16 * MS * WM, TN = 16 * NS * WN;
   g.tiles_n = static_cast<int32_t>((g.n + TN - 1) / TN);
@@ -751,10 +977,10 @@ hipError_t launch_tile(I8Args g, int64_t max_tiles, hipStream_t s) {
     g.tiles_m = static_cast<int32_t>((g.m + TM - 1) / TM);
     grid = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
   } else {
-    grid = max_tiles * ((g.tiles_n + 7) / 8 * 8);
+    grid = (max_tiles + 7) / 8 * 8 * g.tiles_n;
   }
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((i8_tile_kernel<MODE, WM, WN, MS, NS, KB, S, OCC>),
+  hipLaunchKernelGGL((i8_tile_kernel<MODE, WM, WN, MS, NS, KB, S, OCC, PP>),
                      dim3(static_cast<unsigned>(grid)), dim3(64 * WM * WN), 0, s, g);
   return hipGetLastError();
 }
@@ -768,6 +994,43 @@ hipError_t launch_skinny_cfg(I8Args g, int64_t max_tiles, hipStream_t s) {
   hipLaunchKernelGGL((i8_skinny_kernel<MODE, MT, NT, KW, B>), dim3(static_cast<unsigned>(grid)),
                      dim3(64 * KW), 0, s, g);
   return hipGetLastError();
+}
+
+// The dense tile: the one with the least time per 128 bytes of k, from the
+// number of tiles and what each kernel was measured to need.  `alone` is a
+// step's time with one workgroup on a compute unit, `each` what every further
+// one adds, `slots` how many fit; 256 compute units.  (us per step, from
+// sweeps over m = 32 .. 4096 at (k, n) = (2688, 8192), (8192, 2688) and (1856,
+// 2688); the order it gives was that of the measured times at all of them, to
+// within 8 %.)
+int pick_tile(int64_t m, int64_t n) {
+  struct Cost {
+    int tm, tn, slots;
+    double alone, each;
+  };
+  static constexpr Cost kCosts[] = {
+      {32, 32, 4, 0.15, 0.115},  {32, 64, 3, 0.17, 0.17},  {64, 64, 3, 0.235, 0.19},
+      {64, 128, 3, 0.51, 0.28},  {128, 128, 2, 0.59, 0.41}, {192, 256, 1, 1.30, 1.30},
+      {256, 256, 1, 1.35, 1.35},
+  };
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < static_cast<int>(sizeof(kCosts) / sizeof(kCosts[0])); ++i) {
+    const Cost &c = kCosts[i];
+    const int64_t tiles = ((m + c.tm - 1) / c.tm) * ((n + c.tn - 1) / c.tn);
+    const int64_t per_cu = (tiles + 255) / 256;
+    auto step = [&](int64_t w) {
+      const double t = c.each * static_cast<double>(w);
+      return w == 0 ? 0.0 : (t > c.alone ? t : c.alone);
+    };
+    const double cost =
+        static_cast<double>(per_cu / c.slots) * step(c.slots) + step(per_cu % c.slots);
+    if (i == 0 || cost < least) {
+      best = i;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -825,17 +1088,41 @@ hipError_t launch_linear_int8(const int8_t *xq, const float *xs, int64_t m, int6
   const size_t quad = tail.bf16 ? 8 : 16;
   g.vec = n % 4 == 0 && reinterpret_cast<uintptr_t>(y) % quad == 0 &&
           reinterpret_cast<uintptr_t>(tail.residual) % quad == 0;
-  if (m <= 16) return launch_skinny_cfg<kI8Dense, 1, 2, 8, 6>(g, 0, s);
-  if (m <= 32) return launch_skinny_cfg<kI8Dense, 2, 2, 8, 6>(g, 0, s);
-  if (m <= 64) return launch_skinny_cfg<kI8Dense, 4, 1, 8, 4>(g, 0, s);
-  if (m * n < 256 * 128 * 128) return launch_tile<kI8Dense, 2, 2, 2, 2, 128, 3, 2>(g, 0, s);
-  if (m * n < 256 * 256 * 256) return launch_tile<kI8Dense, 2, 2, 4, 4, 128, 2, 2>(g, 0, s);
-  return launch_tile<kI8Dense, 2, 4, 8, 4, 64, 4, 2>(g, 0, s);
+  const int32_t halves = g.kp / kI8Step;
+  // Up to 16 rows and 4096 columns the workgroups of the tile kernel are too
+  // few to pull the weights in, and the register stream, which splits k over
+  // 8 waves, is ahead: 16 x 1856 x 2688 3.7 us against 4.2, 16 x 2688 x 1856
+  // 4.5 against 5.2, 16 x 8192 x 2688 9.7 against 10.2; at 4096 columns they
+  // meet (6.8 against 6.6), and at 8192 the tiles win (7.5 against 6.4 us,
+  // k = 2688).  A wave takes its steps in batches of 6 or, from 7 on, of 8
+  // (k = 8192, n = 2688: 10.4 us in sixes, 9.7 in eights; k = 2688, n = 8192
+  // the other way round, 7.4 and 8.9).
+  if (m <= 16 && n <= 4096) {
+    if (halves <= 8 * 6) return launch_skinny_cfg<kI8Dense, 1, 1, 8, 6>(g, 0, s);
+    return launch_skinny_cfg<kI8Dense, 1, 1, 8, 8>(g, 0, s);
+  }
+  switch (pick_tile(m, n)) {
+    case 0: return launch_tile<kI8Dense, 2, 2, 1, 1, 128, 5, 2>(g, 0, s);
+    case 1: return launch_tile<kI8Dense, 2, 2, 1, 2, 128, 4, 2>(g, 0, s);
+    case 2: return launch_tile<kI8Dense, 2, 2, 2, 2, 128, 3, 2>(g, 0, s);
+    case 3: return launch_tile<kI8Dense, 2, 2, 2, 4, 128, 2, 2>(g, 0, s);
+    case 4: return launch_tile<kI8Dense, 2, 2, 4, 4, 128, 2, 2>(g, 0, s);
+    case 5: return launch_tile<kI8Dense, 2, 4, 6, 4, 128, 2, 2>(g, 0, s);
+    default: return launch_tile<kI8Dense, 2, 4, 8, 4, 64, 4, 2, true>(g, 0, s);
+  }
 }
 
+// Rows per tile by the average number of rows per expert, from sweeps of the
+// two products over 128 experts of 1856 x 2688 (up + down, us; uniform
+// routing, then Zipf): 6 rows 16-row tiles 278 / 260, 64-row tiles 235 / 203;
+// 24 rows 64-row 257 / 277, 128-row 265 / 275; 48 rows 280 / 326 and 287 /
+// 309; 96 rows 128-row 325 / 380, 256-row 354 / 402; 140 rows 460 / 459 and
+// 382 / 469.  At 3 rows 16-row tiles take 226.
 int int8_moe_tile_rows(int64_t pairs, int32_t n_experts) {
-  if (pairs <= 16 * static_cast<int64_t>(n_experts)) return 16;
-  return pairs <= 128 * static_cast<int64_t>(n_experts) ? 64 : 128;
+  const int64_t e = n_experts;
+  if (pairs <= 4 * e) return 16;
+  if (pairs <= 32 * e) return 64;
+  return pairs <= 128 * e ? 128 : 256;
 }
 
 hipError_t launch_moe_int8(int mode, int tile_rows, const int8_t *aq, const float *as,
@@ -857,16 +1144,26 @@ hipError_t launch_moe_int8(int mode, int tile_rows, const int8_t *aq, const floa
   g.n_tiles = n_tiles;
   g.a_rows = a_rows;
   g.topk = topk;
+  // 16-row tiles: a wave's share of the steps (a quarter) in one batch where
+  // it fits (16 tokens: up, 11 steps, 63 us in one batch of 11 and 81-91 in
+  // eights; down, 8 steps, 59 us in eights and 63 in elevens)
+  const bool eights = g.kp <= 4 * 8 * kI8Step;
   switch (tile_rows) {
     case 16:
-      if (mode == 0) return launch_skinny_cfg<kI8Up, 1, 2, 4, 8>(g, max_tiles, s);
-      return launch_skinny_cfg<kI8Down, 1, 2, 4, 8>(g, max_tiles, s);
+      if (mode == 0)
+        return eights ? launch_skinny_cfg<kI8Up, 1, 1, 4, 8>(g, max_tiles, s)
+                      : launch_skinny_cfg<kI8Up, 1, 1, 4, 11>(g, max_tiles, s);
+      return eights ? launch_skinny_cfg<kI8Down, 1, 1, 4, 8>(g, max_tiles, s)
+                    : launch_skinny_cfg<kI8Down, 1, 1, 4, 11>(g, max_tiles, s);
     case 64:
       if (mode == 0) return launch_tile<kI8Up, 1, 4, 4, 2, 128, 3, 2>(g, max_tiles, s);
       return launch_tile<kI8Down, 1, 4, 4, 2, 128, 3, 2>(g, max_tiles, s);
     case 128:
       if (mode == 0) return launch_tile<kI8Up, 2, 4, 4, 4, 128, 3, 2>(g, max_tiles, s);
       return launch_tile<kI8Down, 2, 4, 4, 4, 128, 3, 2>(g, max_tiles, s);
+    case 256:
+      if (mode == 0) return launch_tile<kI8Up, 2, 4, 8, 4, 128, 2, 2>(g, max_tiles, s);
+      return launch_tile<kI8Down, 2, 4, 8, 4, 128, 2, 2>(g, max_tiles, s);
     default: return hipErrorInvalidValue;
   }
 }
