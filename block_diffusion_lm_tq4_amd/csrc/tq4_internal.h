@@ -362,6 +362,7 @@ struct RouterConfig {
   int32_t n_groups, topk_groups;
   int32_t renormalize;
   float scale;
+  uint32_t per_inv;    // set by the launcher: 2^20 / (experts per group), rounded up
 };
 hipError_t launch_router_scored(const float *logits, int64_t t, const RouterConfig &cfg,
                                 const float *bias, int32_t *ids, float *w, hipStream_t s);
