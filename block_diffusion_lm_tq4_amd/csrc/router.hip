@@ -32,29 +32,92 @@ constexpr float kNoneF = -__builtin_inff();
 // ---- one token by one wave, all in fp64 -------------------------------------
 // Any number of groups and slots.  Lane l holds experts l, l + 64, ...
 
-__device__ inline double wave_max(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = __builtin_fmax(v, __shfl_xor(v, d));
-  return v;
+template <int CTRL>
+__device__ inline float dpp_f(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ inline int dpp_i(int v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ inline double dpp_d(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = dpp_i<CTRL>(static_cast<int>(b));
+  const uint32_t hi = dpp_i<CTRL>(static_cast<int>(b >> 32));
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
+// The values of lanes l and l ^ 16 (or l ^ 32), lower lane first.
+template <int D>
+__device__ inline void lane_pair_f64(double v, double &lower, double &upper) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  uint32_t l0, u0, l1, u1;
+  if constexpr (D == 16) {
+    lane_pair16(static_cast<uint32_t>(b), l0, u0);
+    lane_pair16(static_cast<uint32_t>(b >> 32), l1, u1);
+  } else {
+    lane_pair32(static_cast<uint32_t>(b), l0, u0);
+    lane_pair32(static_cast<uint32_t>(b >> 32), l1, u1);
+  }
+  lower = __builtin_bit_cast(double, static_cast<uint64_t>(l1) << 32 | l0);
+  upper = __builtin_bit_cast(double, static_cast<uint64_t>(u1) << 32 | u0);
+}
+
+// Wave-wide reductions in registers: partners l ^ 1, l ^ 2, 7 - l and 15 - l
+// within a row of 16 lanes, then l ^ 16 and l ^ 32; each combine commutative, so
+// every lane ends with the same result.
+template <class F>
+__device__ inline double row_reduce_f64(double v, F f) {
+  v = f(v, dpp_d<0xB1>(v));
+  v = f(v, dpp_d<0x4E>(v));
+  v = f(v, dpp_d<0x141>(v));
+  return f(v, dpp_d<0x140>(v));
+}
+template <class F>
+__device__ inline double wave_reduce_f64(double v, F f) {
+  v = row_reduce_f64(v, f);
+  double lo, hi;
+  lane_pair_f64<16>(v, lo, hi);
+  v = f(lo, hi);
+  lane_pair_f64<32>(v, lo, hi);
+  return f(lo, hi);
+}
+__device__ inline double wave_max(double v) {
+  return wave_reduce_f64(v, [](double a, double b) { return __builtin_fmax(a, b); });
+}
 __device__ inline double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  return wave_reduce_f64(v, [](double a, double b) { return a + b; });
+}
+__device__ inline double row_sum_f64(double v) {
+  return row_reduce_f64(v, [](double a, double b) { return a + b; });
 }
 
 // The largest (value, index) over the wave, ties to the lower index.
-__device__ inline void wave_best(double &v, int &i) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double ov = __shfl_xor(v, d);
-    const int oi = __shfl_xor(i, d);
-    if (ov > v || (ov == v && oi < i)) {
-      v = ov;
-      i = oi;
-    }
+__device__ inline void better_f64(double &v, int &i, double ov, int oi) {
+  if (ov > v || (ov == v && oi < i)) {
+    v = ov;
+    i = oi;
   }
+}
+__device__ inline void wave_best(double &v, int &i) {
+  better_f64(v, i, dpp_d<0xB1>(v), dpp_i<0xB1>(i));
+  better_f64(v, i, dpp_d<0x4E>(v), dpp_i<0x4E>(i));
+  better_f64(v, i, dpp_d<0x141>(v), dpp_i<0x141>(i));
+  better_f64(v, i, dpp_d<0x140>(v), dpp_i<0x140>(i));
+  double vl, vh;
+  uint32_t il, ih;
+  lane_pair_f64<16>(v, vl, vh);
+  lane_pair16(static_cast<uint32_t>(i), il, ih);
+  v = vl;
+  i = static_cast<int>(il);
+  better_f64(v, i, vh, static_cast<int>(ih));
+  lane_pair_f64<32>(v, vl, vh);
+  lane_pair32(static_cast<uint32_t>(i), il, ih);
+  v = vl;
+  i = static_cast<int>(il);
+  better_f64(v, i, vh, static_cast<int>(ih));
 }
 
 // A wave's LDS writes before its later reads.
@@ -210,41 +273,29 @@ __global__ __launch_bounds__(256) void router_f64_kernel(
 
 // ---- four tokens by one wave, decided in fp32 where that decides --------------
 // Sixteen lanes (a DPP row) per token, lane l with the P experts l P ... .
-// Choice values are formed in fp32.  Their errors: a score comes from exp2 of a
-// rounded product, so it is off by 2^-24 |x| p for the exponent x (l, or l - top
-// for a softmax) and a few steps more; added to a bias, by 2^-24 |c| more.
-// Relative to the token's largest score pmax that is at most 2^-20 + 2^-23
-// |top| (p |l| is largest at the top for negative logits, and at most 0.28
-// otherwise; p (top - l) is at most pmax / e).
-// The topk + 1 largest are found with ties to the lower id.  If each is further
-// from the next than both errors, or, among the chosen, has the very same logit
-// and bias (then so are the exact values, and the lower id is right), their
-// order is the exact one.  Groups likewise: only the border between the kept
-// and the others has to be clear, of sums of two.  A token that fails a test
-// (about 1 in 300 of random ones) is done again by route_token_f64.  Weights
-// are formed from the chosen logits in fp64; only a softmax without
-// renormalization needs all of them for that.
+// Choice values c are formed in fp32, and each becomes one integer that orders
+// like it, its last 6 to 9 bits given to the expert (ties to the lower id), so
+// that the largest of a token is found by integer maxima alone.  The topk + 2
+// largest are candidates; their exact values (which the weights need anyway)
+// are formed in fp64, one in each lane, and where two neighbours among them are
+// near, the candidates are ranked by those.  The choice is then the exact one if
+// the last candidate, above which no other expert is, lies clear of the last
+// chosen by the fp32 values.  Groups likewise: the border between the kept and
+// the others has to be clear.  A token that fails either test (about 1 in
+// 15000 of random ones) is done again by route_token_f64.
+//
+// "Clear" is more than both errors.  exp_fast is off by 2^-23 + 1.5 * 2^-24 |x|
+// of itself.  A sigmoid score adds 1 + e and the reciprocal, 1.5 * 2^-23 more;
+// with p (1 - p) |l| at most 0.23, or |l| p where the token's top logit is
+// negative, that is at most pmax 2^-23 (3 + max(0, -top)), pmax the largest
+// score.  A softmax score has the rounding of l - top as well, p (top - l) is
+// at most pmax / e, and the sum's error is common to the token: at most 18 *
+// 2^-23 pmax.  Adding the bias costs 2^-24 |c|.  Without a bias the errors are
+// taken relative to the value itself.  Dropping B bits costs 2^(B - 23) |c|.
+//
 // Bound by its instructions, not by the logits' bytes.
 
-template <int CTRL>
-__device__ inline float dpp_f(float v) {
-  return __builtin_bit_cast(
-      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
-}
-template <int CTRL>
-__device__ inline int dpp_i(int v) {
-  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, false);
-}
-template <int CTRL>
-__device__ inline double dpp_d(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = dpp_i<CTRL>(static_cast<int>(b));
-  const uint32_t hi = dpp_i<CTRL>(static_cast<int>(b >> 32));
-  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-
-// Over the 16 lanes of a row: partners l ^ 1, l ^ 2, 7 - l and 15 - l, each
-// combine commutative, so every lane ends with the same result.
+// Over the 16 lanes of a row, as above.
 template <class F>
 __device__ inline float row_reduce(float v, F f) {
   v = f(v, dpp_f<0xB1>(v));
@@ -258,43 +309,45 @@ __device__ inline float row_max(float v) {
 __device__ inline float row_sum(float v) {
   return row_reduce(v, [](float a, float b) { return a + b; });
 }
-__device__ inline double row_sum_f64(double v) {
-  v += dpp_d<0xB1>(v);
-  v += dpp_d<0x4E>(v);
-  v += dpp_d<0x141>(v);
-  return v + dpp_d<0x140>(v);
-}
-__device__ inline int row_min(int v) {
+__device__ inline int row_max_i(int v) {
   int o = dpp_i<0xB1>(v);
-  v = o < v ? o : v;
+  v = o > v ? o : v;
   o = dpp_i<0x4E>(v);
-  v = o < v ? o : v;
+  v = o > v ? o : v;
   o = dpp_i<0x141>(v);
-  v = o < v ? o : v;
+  v = o > v ? o : v;
   o = dpp_i<0x140>(v);
-  return o < v ? o : v;
+  return o > v ? o : v;
 }
 
 constexpr int kFastGroups = 16;  // groups the row's lanes hold
-constexpr int kFastSlots = 15;   // slots, with the runner-up in one more lane
+constexpr int kFastSlots = 14;   // slots, with two more candidates in the lanes left
 
-// exp(x), off by at most (2^-24 |x| + 2^-22) of itself.
+// exp(x), off by at most (1.5 * 2^-24 |x| + 2^-23) of itself.
 __device__ inline float exp_fast(float x) {
   return __builtin_amdgcn_exp2f(x * 0x1.715476p+0f);
 }
 
+// (Workgroups of one wave took 26 us for 16411 tokens of 256 experts: 4103 of
+// them are dispatched no faster.)
+constexpr int kFastWaves = 4;
+
 template <int P>
-__global__ __launch_bounds__(64) void router_fast_kernel(
+__global__ __launch_bounds__(64 * kFastWaves) void router_fast_kernel(
     const float *__restrict__ logits, int64_t t, RouterConfig cfg,
     const float *__restrict__ bias, int32_t *__restrict__ ids, float *__restrict__ w) {
   // four tokens' choice values where groups do not fall on lanes; the fp64
   // pass uses the space afterwards
   constexpr int kRow = 16 * P + 1;
   constexpr int kBytes = 4 * kRow * 4 > kMaxExperts * 8 ? 4 * kRow * 4 : kMaxExperts * 8;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kBytes];
-  const int lane = threadIdx.x;
+  __shared__ __attribute__((aligned(16))) uint8_t all[kFastWaves][(kBytes + 15) / 16 * 16];
+  uint8_t *smem = all[threadIdx.x / 64];
+  const int lane = threadIdx.x % 64;
   const int l16 = lane % 16;
-  const int64_t tok_raw = static_cast<int64_t>(blockIdx.x) * 4 + lane / 16;
+  // the wave's first token
+  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * (4 * kFastWaves) + threadIdx.x / 64 * 4;
+  if (tok0 >= t) return;
+  const int64_t tok_raw = tok0 + lane / 16;
   const bool real = tok_raw < t;
   const int64_t tok = real ? tok_raw : t - 1;  // spare rows repeat the last token
   const int n = cfg.n_experts;
@@ -377,7 +430,9 @@ __global__ __launch_bounds__(64) void router_fast_kernel(
   cmax = row_max(cmax);
   // the error of one choice value, at most (infinite if a bias is: then the
   // token is left to fp64)
-  const float err = pmax * (0x1p-20f + 0x1p-23f * __builtin_fabsf(m)) + 0x1p-23f * cmax + 0x1p-110f;
+  const float err =
+      pmax * 0x1p-23f * (cfg.sigmoid ? 3.f + __builtin_fmaxf(0.f, -m) : 18.f) +
+      0x1p-24f * cmax + 0x1p-110f;
   bool clear = err < __builtin_inff();
 
   if (cfg.n_groups > 1) {
@@ -411,11 +466,11 @@ __global__ __launch_bounds__(64) void router_fast_kernel(
     const float gs = b > kNoneF ? a + b : a;
     // a group's rank: how many come before it (row_ror:s brings lane l - s)
     const int step = on_lanes ? span : 1;
-    const int mine = l16 / step;
+    const int own = l16 / step;
     int rank = 0;
     auto before = [&](float o, int s) __attribute__((always_inline)) {
       const int j = ((l16 - s) & 15) / step;
-      rank += (o > gs || (o == gs && j < mine)) ? 1 : 0;
+      rank += (o > gs || (o == gs && j < own)) ? 1 : 0;
     };
     if (step < 2) {
       before(dpp_f<0x121>(gs), 1);
@@ -442,7 +497,7 @@ __global__ __launch_bounds__(64) void router_fast_kernel(
     const float last = -row_max(keep ? -gs : kNoneF);
     const float next = row_max(keep ? kNoneF : gs);
     // (no group kept, or no other left: last or next is infinite)
-    clear = clear && last - next > 2.f * (2.f * err + 0x1p-23f * cmax);
+    clear = clear && last - next > 2.f * (2.f * err + 0x1p-23f * cmax);  // sums of two
     if (on_lanes) {
 #pragma unroll
       for (int i = 0; i < P; ++i) c[i] = keep ? c[i] : kNoneF;
@@ -457,70 +512,102 @@ __global__ __launch_bounds__(64) void router_fast_kernel(
     }
   }
 
-  // the topk + 1 largest, result j in lane j of the row
-  float my_c = kNoneF;
-  int my_id = -1;
-  for (int j = 0; j <= cfg.topk; ++j) {
-    float best = c[0];
+  // keys: integers in the order of the values, the last kBits the expert
+  constexpr int kBits = P == 4 ? 6 : (P == 8 ? 7 : (P == 16 ? 8 : 9));
+  constexpr int kMask = (1 << kBits) - 1;
+  constexpr int kNoKey = -0x7FFFFFFF - 1;
+  int key[P];
 #pragma unroll
-    for (int i = 1; i < P; ++i) best = __builtin_fmaxf(best, c[i]);
-    best = row_max(best);
-    int pos = P;  // the lane's lowest position of it
-#pragma unroll
-    for (int i = P - 1; i >= 0; --i) pos = c[i] == best ? i : pos;
-    const int at = row_min(pos < P ? e0 + pos : 0x7FFFFFFF);
-    if (l16 == j && best > kNoneF) {
-      my_c = best;
-      my_id = at;
-    }
-    const int gone = at - e0;
-#pragma unroll
-    for (int i = 0; i < P; ++i) c[i] = i == gone ? kNoneF : c[i];
+  for (int i = 0; i < P; ++i) {
+    const int bits = __builtin_bit_cast(int, c[i]);
+    const int ordered = bits ^ ((bits >> 31) & 0x7FFFFFFF);
+    key[i] = c[i] > kNoneF ? (ordered & ~kMask) | (kMask - (e0 + i)) : kNoKey;
   }
-
-  // each result against the next one (row_shl:1 brings lane l + 1)
-  const bool found = my_id >= 0;
-  const float my_l = found ? row[my_id] : 0.f;
+  // the topk + 2 largest, candidate j in lane j of the row
+  int mine = kNoKey;
+  for (int j = 0; j < cfg.topk + 2; ++j) {
+    int best = key[0];
+#pragma unroll
+    for (int i = 1; i < P; ++i) best = key[i] > best ? key[i] : best;
+    best = row_max_i(best);
+    mine = l16 == j ? best : mine;
+#pragma unroll
+    for (int i = 0; i < P; ++i) key[i] = key[i] == best ? kNoKey : key[i];
+  }
+  const bool found = mine != kNoKey;
+  const int my_id = found ? kMask - (mine & kMask) : -1;
+  const int cut = mine & ~kMask;
+  const float my_c =
+      found ? __builtin_bit_cast(float, cut ^ ((cut >> 31) & 0x7FFFFFFF)) : kNoneF;
+  const float my_l = found ? __builtin_fminf(row[my_id], 3.402823466e38f) : 0.f;
   const float my_b = found && bias != nullptr ? bias[my_id] : 0.f;
-  const float next_c = dpp_f<0x101>(my_c);
-  const float next_l = dpp_f<0x101>(my_l);
-  const float next_b = dpp_f<0x101>(my_b);
-  const int next_id = dpp_i<0x101>(my_id);
-  // without a bias the errors are relative to the values themselves (for a
-  // softmax, that of l - top as well)
-  const float tol = bias != nullptr
-                        ? 2.f * err
-                        : my_c * (0x1p-18f + 0x1p-21f * (cfg.sigmoid ? __builtin_fabsf(my_l) : top - my_l));
-  const bool apart = my_c - next_c > tol && (bias != nullptr || my_c > 0x1p-100f);
-  // at the last slot equal inputs do not settle it: a third expert may be near
-  const bool equal = my_l == next_l && my_b == next_b && l16 + 1 < cfg.topk;
-  if (l16 < cfg.topk && found && next_id >= 0 && !apart && !equal) clear = false;
 
-  // weights of the chosen, in fp64
-  const bool chosen = found && l16 < cfg.topk;
-  const double dl = static_cast<double>(__builtin_fminf(my_l, 3.402823466e38f));
+  // the distance below which two values are near
+  constexpr float kDrop = 1.f / static_cast<float>(1 << (23 - kBits));
+  const float tol =
+      bias != nullptr
+          ? 2.f * err + kDrop * cmax
+          : my_c * (kDrop + 0x1p-18f + 0x1p-21f * (cfg.sigmoid ? __builtin_fabsf(my_l) : m - my_l));
+  const bool tiny = bias == nullptr && !(my_c > 0x1p-100f);
+  const float next_c = dpp_f<0x101>(my_c);   // lane l + 1
+  const float after_c = dpp_f<0x102>(my_c);  // lane l + 2
+  // among the chosen and the first after them
+  const bool near = found && l16 < cfg.topk && (tiny || !(my_c - next_c > tol));
+  // the last chosen against the last candidate
+  if (found && l16 == cfg.topk - 1 && after_c > kNoneF && (tiny || !(my_c - after_c > tol)))
+    clear = false;
+
+  // the candidates' scores in fp64
+  const double dl = static_cast<double>(my_l);
   double p = 0.0;
   if (cfg.sigmoid) {
-    if (chosen) p = 1.0 / (1.0 + exp(-dl));
+    if (found) p = 1.0 / (1.0 + exp(-dl));
   } else {
-    if (chosen) p = exp(dl - static_cast<double>(top));
-    if (!cfg.renormalize) {
+    if (found) p = exp(dl - static_cast<double>(m));
+    if (!cfg.renormalize || bias != nullptr) {
       double sum = 0.0;
 #pragma unroll
       for (int i = 0; i < P; ++i)
-        sum += l[i] > kNoneF ? exp(static_cast<double>(l[i]) - static_cast<double>(top)) : 0.0;
+        sum += l[i] > kNoneF ? exp(static_cast<double>(l[i]) - static_cast<double>(m)) : 0.0;
       sum = row_sum_f64(sum);
-      if (chosen) p /= sum;
+      if (found) p /= sum;
     }
   }
+  int slot = l16;
+  if (__any(near)) {
+    // ranks by the exact values, ties to the lower id
+    const double d = found ? p + static_cast<double>(my_b) : kNone;
+    slot = 0;
+    auto count = [&](double od, int oid) __attribute__((always_inline)) {
+      slot += (od > d || (od == d && oid < my_id)) ? 1 : 0;
+    };
+    count(dpp_d<0x121>(d), dpp_i<0x121>(my_id));
+    count(dpp_d<0x122>(d), dpp_i<0x122>(my_id));
+    count(dpp_d<0x123>(d), dpp_i<0x123>(my_id));
+    count(dpp_d<0x124>(d), dpp_i<0x124>(my_id));
+    count(dpp_d<0x125>(d), dpp_i<0x125>(my_id));
+    count(dpp_d<0x126>(d), dpp_i<0x126>(my_id));
+    count(dpp_d<0x127>(d), dpp_i<0x127>(my_id));
+    count(dpp_d<0x128>(d), dpp_i<0x128>(my_id));
+    count(dpp_d<0x129>(d), dpp_i<0x129>(my_id));
+    count(dpp_d<0x12A>(d), dpp_i<0x12A>(my_id));
+    count(dpp_d<0x12B>(d), dpp_i<0x12B>(my_id));
+    count(dpp_d<0x12C>(d), dpp_i<0x12C>(my_id));
+    count(dpp_d<0x12D>(d), dpp_i<0x12D>(my_id));
+    count(dpp_d<0x12E>(d), dpp_i<0x12E>(my_id));
+    count(dpp_d<0x12F>(d), dpp_i<0x12F>(my_id));
+    if (!found) slot = l16;  // the lanes behind the candidates keep their places
+  }
+  const bool chosen = slot < cfg.topk;
+  if (!found) p = 0.0;
   double f = static_cast<double>(cfg.scale);
   if (cfg.renormalize) {
-    const double total = row_sum_f64(p);
+    const double total = row_sum_f64(chosen ? p : 0.0);
     f = total > 0.0 ? f / total : 0.0;
   }
-  if (real && l16 < cfg.topk) {
-    ids[tok * cfg.topk + l16] = my_id;
-    w[tok * cfg.topk + l16] = static_cast<float>(p * f);
+  if (real && chosen) {
+    ids[tok * cfg.topk + slot] = my_id;
+    w[tok * cfg.topk + slot] = static_cast<float>(p * f);
   }
 
   // unclear tokens again, one after another, by the whole wave
@@ -528,7 +615,7 @@ __global__ __launch_bounds__(64) void router_fast_kernel(
   while (again != 0) {
     const int first = __builtin_ctzll(again) & 48;
     again &= ~(0xFFFFull << first);
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + first / 16;
+    const int64_t at = tok0 + first / 16;
     wave_lds_fence();
     route_token_f64<P / 4, 1>(logits + at * n, cfg, bias, reinterpret_cast<double *>(smem), lane,
                     ids + at * cfg.topk, w + at * cfg.topk);
@@ -548,16 +635,18 @@ hipError_t launch_router_scored(const float *logits, int64_t t, const RouterConf
                        s, logits, t, cfg, bias, ids, w);
     return hipGetLastError();
   }
-  const dim3 grid(static_cast<unsigned>((t + 3) / 4));
+  constexpr int64_t kTokens = 4 * kFastWaves;
+  const dim3 grid(static_cast<unsigned>((t + kTokens - 1) / kTokens));
+  const dim3 block(64 * kFastWaves);
   if (cfg.n_experts <= 64)
-    hipLaunchKernelGGL(router_fast_kernel<4>, grid, dim3(64), 0, s, logits, t, cfg, bias, ids, w);
+    hipLaunchKernelGGL(router_fast_kernel<4>, grid, block, 0, s, logits, t, cfg, bias, ids, w);
   else if (cfg.n_experts <= 128)
-    hipLaunchKernelGGL(router_fast_kernel<8>, grid, dim3(64), 0, s, logits, t, cfg, bias, ids, w);
+    hipLaunchKernelGGL(router_fast_kernel<8>, grid, block, 0, s, logits, t, cfg, bias, ids, w);
   else if (cfg.n_experts <= 256)
-    hipLaunchKernelGGL(router_fast_kernel<16>, grid, dim3(64), 0, s, logits, t, cfg, bias, ids,
+    hipLaunchKernelGGL(router_fast_kernel<16>, grid, block, 0, s, logits, t, cfg, bias, ids,
                        w);
   else
-    hipLaunchKernelGGL(router_fast_kernel<32>, grid, dim3(64), 0, s, logits, t, cfg, bias, ids,
+    hipLaunchKernelGGL(router_fast_kernel<32>, grid, block, 0, s, logits, t, cfg, bias, ids,
                        w);
   return hipGetLastError();
 }
