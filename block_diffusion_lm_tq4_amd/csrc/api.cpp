@@ -681,6 +681,10 @@ int linear_int8_impl(const uint16_t *x_bf16, const int8_t *x_codes, const float 
   if (!aligned(cache, 16)) return TQ4_E_ALIGN;
   if (x_bf16 != nullptr) {
     if (!aligned(x_bf16, 16)) return TQ4_E_ALIGN;
+    if (tq4::int8_direct_fits(m, k))
+      return device_status(tq4::launch_linear_int8_direct(
+          x_bf16, m, k, reinterpret_cast<const int8_t *>(cache), int8_scales(cache, n, k), n, tail,
+          y, s));
     const int ws = check_workspace(workspace, workspace_bytes,
                                    tq4_linear_int8_workspace_size(m, k, n));
     if (ws != TQ4_OK) return ws;
@@ -750,7 +754,7 @@ int tq4_act_int8(const uint16_t *x_bf16, int64_t m, int64_t k, int8_t *codes, fl
 
 size_t tq4_linear_int8_workspace_size(int64_t m, int64_t k, int64_t n) {
   if (!int8_sizes_ok(m, k) || !int8_sizes_ok(n, k)) return 0;
-  if (m == 0 || n == 0 || k == 0) return 0;
+  if (m == 0 || n == 0 || k == 0 || tq4::int8_direct_fits(m, k)) return 0;
   return align_up(int8_codes_bytes(m, k)) + align_up(static_cast<size_t>(m) * sizeof(float));
 }
 
@@ -862,6 +866,12 @@ int tq4_moe_grouped_int8(const uint16_t *x_bf16, int64_t t, int64_t k, const int
   const int64_t pairs = t * topk;
   const int64_t e64 = n_experts;
   hipStream_t s = as_stream(stream);
+  if (tq4::int8_moe_direct_fits(t, topk, n1, k))
+    return device_status(tq4::launch_moe_int8_direct(
+        x_bf16, t, k, topk_ids, topk_w, topk, n_experts,
+        reinterpret_cast<const int8_t *>(w1_cache), int8_scales(w1_cache, e64 * n1, k), n1,
+        reinterpret_cast<const int8_t *>(w2_cache), int8_scales(w2_cache, e64 * k, n1), h, out,
+        s));
   hipError_t e = tq4::launch_act_int8(x_bf16, t, k, xq, xs, s);
   if (e == hipSuccess)
     e = tq4::launch_route(topk_ids, pairs, topk, n_experts, counts, offsets, perm, inv, tiles,

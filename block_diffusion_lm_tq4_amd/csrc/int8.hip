@@ -35,6 +35,13 @@ typedef int intx4 __attribute__((ext_vector_type(4)));
 
 constexpr int kI8Step = 64;
 
+// A wave's LDS writes before its later reads (nothing but the compiler could
+// change their order).
+__device__ inline void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // ---------------------------------------------------------------------------
 // Rows to codes
 
@@ -55,64 +62,75 @@ __device__ inline T group_max(T v, T *red) {
   return m;
 }
 
-// Eight codes of one 16-byte piece of a bf16 row.  The quotient 127 v / a is
-// taken as (127 v) * rcp(a), off by at most 2^(-15-d) (d as above): it rounds
-// like the exact one unless that is a half-integer.  Then, and only then, the
-// remainder 127 v - q a (exact in one fma: both terms are multiples of v's
-// last bit, and it is at most a / 2) is plus or minus a / 2, and the even
-// neighbour is taken.  11 instead of about 20 instructions for each code.
-__device__ inline uint2 codes_of(uint4 d, float sc, float a, float inv) {
-  const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-  uint32_t out[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t word = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t pair = w[2 * h + j / 2];
-      const float v = __uint_as_float(j % 2 ? pair & 0xFFFF0000u : pair << 16);
-      const float p = (v * sc) * 127.f;
-      const float q = __builtin_rintf(p * inv);
-      const float rho = __builtin_fmaf(-q, a, p);
-      int qi = static_cast<int>(q);
-      if ((qi & 1) && __builtin_fabsf(rho) + __builtin_fabsf(rho) == a) qi += rho > 0.f ? 1 : -1;
-      word |= (static_cast<uint32_t>(qi) & 0xFFu) << (8 * j);
-    }
-    out[h] = word;
-  }
-  return make_uint2(out[0], out[1]);
-}
-
-// The largest magnitude bits of a piece.  Magnitude bits of bf16 order like
-// the magnitudes, infinities and NaN last (0x7F80 and above).
-__device__ inline uint32_t top_of(uint4 d) {
-  const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-  uint32_t t = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
-    t = t > lo ? t : lo;
-    t = t > hi ? t : hi;
-  }
-  return t;
-}
-
 // What a row's largest magnitude bits say about it.
 struct RowScale {
-  float sc, a, inv, scale;
+  float c127, inv, a, half, scale;
   bool live;
   __device__ explicit RowScale(uint32_t top) {
     // a power of two that keeps 127 v and 1 / a in range; it changes no
     // quotient: what the smaller one could drop has the code 0
-    sc = top >= 0x7000u ? 0x1p-8f : (top < 0x1000u ? 0x1p+96f : 1.f);
+    const float sc = top >= 0x7000u ? 0x1p-8f : (top < 0x1000u ? 0x1p+96f : 1.f);
     const float amax = __uint_as_float(top << 16);
+    c127 = sc * 127.f;
     a = amax * sc;
+    half = 0.5f * a;
     inv = __builtin_amdgcn_rcpf(a);
     const bool finite = top < 0x7F80u;
     live = finite && top != 0;
     scale = finite ? amax / 127.f : __builtin_nanf("");
   }
 };
+
+// Eight codes of one 16-byte piece of a bf16 row.  fma(127 v, 1 / a, 1.5 * 2^23)
+// rounds the quotient to an integer, whose code is the low byte of the result:
+// one rounding of a value that is off by at most 2^-23 of itself, so it is the
+// exact quotient's unless that is a half-integer (see above).  Then, and only
+// then, the remainder 127 v - q a (exact in one fma: both terms are multiples of
+// v's last bit, and it is at most a / 2) is plus or minus a / 2, and the even
+// neighbour is taken.  Seven instructions for a code, the piece's ties apart;
+// with a division it was about 20.
+__device__ inline uint2 codes_of(uint4 d, const RowScale &rs) {
+  constexpr float kMagic = 12582912.f;
+  const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+  float t[8], rho[8];
+  bool tie = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float v = __uint_as_float(j % 2 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+    const float p = v * rs.c127;
+    t[j] = __builtin_fmaf(p, rs.inv, kMagic);
+    rho[j] = __builtin_fmaf(kMagic - t[j], rs.a, p);
+    tie |= __builtin_fabsf(rho[j]) == rs.half;
+  }
+  if (__builtin_expect(tie, 0)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (__builtin_fabsf(rho[j]) == rs.half && (__float_as_uint(t[j]) & 1u))
+        t[j] += rho[j] > 0.f ? 1.f : -1.f;
+  }
+  uint32_t out[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(t[4 * h + 1]),
+                                              __float_as_uint(t[4 * h]), 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(t[4 * h + 3]),
+                                              __float_as_uint(t[4 * h + 2]), 0x04000C0Cu);
+    out[h] = lo | hi;
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+// The largest magnitude bits of a piece, the even and the odd values apart.
+// Magnitude bits of bf16 order like the magnitudes, infinities and NaN last
+// (0x7F80 and above).
+typedef uint16_t ushortx2 __attribute__((ext_vector_type(2)));
+
+__device__ inline ushortx2 top_of(uint4 d) {
+  auto mag = [](uint32_t w) { return __builtin_bit_cast(ushortx2, w & 0x7FFF7FFFu); };
+  return __builtin_elementwise_max(__builtin_elementwise_max(mag(d.x), mag(d.y)),
+                                   __builtin_elementwise_max(mag(d.z), mag(d.w)));
+}
+__device__ inline uint32_t top_of(ushortx2 t) { return t[0] > t[1] ? t[0] : t[1]; }
 
 // bf16 rows, T threads each (64: a wave per row, four rows per workgroup, no
 // barrier; 256: the workgroup).  A row of up to T * 8 * V values stays in
@@ -133,21 +151,17 @@ __global__ __launch_bounds__(kQThreads) void act_int8_kernel(const uint16_t *__r
     const uint4 *xr = reinterpret_cast<const uint4 *>(x + row * k);
     uint2 *qr = reinterpret_cast<uint2 *>(codes + row * kp);
     uint4 d[V];
-    uint32_t top = 0;
+    ushortx2 tops = {0, 0};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int at = tid + T * i;
       d[i] = at < n_vec ? xr[at] : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t t = top_of(d[i]);
-      top = top > t ? top : t;
-    }
-    for (int at = tid + T * V; at < n_vec; at += T) {
-      const uint32_t t = top_of(xr[at]);
-      top = top > t ? top : t;
-    }
+    for (int i = 0; i < V; ++i) tops = __builtin_elementwise_max(tops, top_of(d[i]));
+    for (int at = tid + T * V; at < n_vec; at += T)
+      tops = __builtin_elementwise_max(tops, top_of(xr[at]));
+    uint32_t top = top_of(tops);
     if constexpr (T == 64) {
 #pragma unroll
       for (int s = 1; s < 64; s <<= 1) {
@@ -163,10 +177,10 @@ __global__ __launch_bounds__(kQThreads) void act_int8_kernel(const uint16_t *__r
     for (int i = 0; i < V; ++i) {
       const int at = tid + T * i;
       if (at < n_out)
-        qr[at] = rs.live ? codes_of(d[i], rs.sc, rs.a, rs.inv) : make_uint2(0u, 0u);
+        qr[at] = rs.live ? codes_of(d[i], rs) : make_uint2(0u, 0u);
     }
     for (int at = tid + T * V; at < n_out; at += T)
-      qr[at] = rs.live && at < n_vec ? codes_of(xr[at], rs.sc, rs.a, rs.inv) : make_uint2(0u, 0u);
+      qr[at] = rs.live && at < n_vec ? codes_of(xr[at], rs) : make_uint2(0u, 0u);
     if (tid == 0) scales[row] = rs.scale;
   }
 }
@@ -555,6 +569,203 @@ __global__ __launch_bounds__(64 * KW) void i8_skinny_kernel(I8Args g) {
           store_moe<MODE>(g, acc[i][j], m0 + 16 * i + r, n0 + 16 * j + 4 * grp, g.xs[src[i]], sw);
     }
   }
+}
+
+// ---- single tokens ------------------------------------------------------------
+// One row: the product needs less time than the launch that would quantize its
+// input, so each wave does that for itself.  It requests the whole row (a few
+// KB, from the caches after the first wave), its own share of it and then its
+// weights, finds the row's largest magnitude and turns its share of k into
+// codes, in its own LDS and without a barrier, while the weights are on their
+// way (loads return in order, so the row's have to come first).  The product
+// is that of the register stream above, the row's codes broadcast to all
+// sixteen rows of the operand.
+//
+// m = 1, 2688 x 8192: 8.3 us against 9.0 for quantizer and product one after
+// the other, and one launch for the host instead of two (8.3 against 12.2 us
+// a call).  From two rows on the wave's own quantization costs more than it
+// saves (10.2 against 9.1 us).
+
+constexpr int kDirectVecs = 16;   // pieces of 8 values per lane: k <= 8192
+constexpr int kDirectSteps = 16;  // steps of 64 k per wave
+
+// A wave's row: request(), then other loads, then finish(), which leaves the
+// codes of steps [s0, s1) in `codes` and returns what the row's maximum says.
+template <int V>
+struct DirectRow {
+  uint4 all[V], own[2];
+  int n_vec, v0, v1;
+
+  __device__ void request(const uint16_t *row, int k, int s0, int s1, int lane) {
+    const uint4 *xr = reinterpret_cast<const uint4 *>(row);
+    n_vec = k / 8;
+    v0 = 8 * s0;
+    v1 = 8 * s1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int at = lane + 64 * i;
+      all[i] = xr[at < n_vec ? at : n_vec - 1];  // a repeat changes no maximum
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = v0 + lane + 64 * i;
+      own[i] = xr[at < n_vec ? at : n_vec - 1];
+    }
+  }
+
+  __device__ RowScale finish(uint8_t *codes, int lane) const {
+    ushortx2 tops = top_of(all[0]);
+#pragma unroll
+    for (int i = 1; i < V; ++i) tops = __builtin_elementwise_max(tops, top_of(all[i]));
+    uint32_t top = top_of(tops);
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const uint32_t o = __shfl_xor(top, s);
+      top = top > o ? top : o;
+    }
+    const RowScale rs(top);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = v0 + lane + 64 * i;
+      if (at < v1)
+        *reinterpret_cast<uint2 *>(codes + 8 * (at - v0)) =
+            rs.live && at < n_vec ? codes_of(own[i], rs) : make_uint2(0u, 0u);
+    }
+    wave_lds_fence();
+    return rs;
+  }
+};
+
+struct I8Direct {
+  const uint16_t *x;   // bf16 rows of k: the input (dense, up) or the hidden rows (down)
+  int32_t k;
+  const int32_t *ids;  // MoE: [t][topk]
+  const float *gates;
+  int32_t n_experts;
+};
+
+// The sum over steps [s0, s1) of one wave: weights already in a[] for the first
+// B steps.
+template <int B>
+__device__ inline void direct_load(intx4 (&a)[B], const int8_t *wp, int s, int s1) {
+#pragma unroll
+  for (int u = 0; u < B; ++u) {
+    const int at = s + u < s1 ? s + u : (s1 > 0 ? s1 - 1 : 0);
+    a[u] = *reinterpret_cast<const intx4 *>(wp + static_cast<int64_t>(at) * kI8Step);
+  }
+}
+
+template <int B>
+__device__ inline intx4 direct_sum(intx4 (&a)[B], const int8_t *wp, const uint8_t *codes, int s0,
+                                   int s1) {
+  intx4 acc = {0, 0, 0, 0};
+  for (int s = s0; s < s1; s += B) {
+    if (s > s0) direct_load<B>(a, wp, s, s1);
+#pragma unroll
+    for (int u = 0; u < B; ++u)
+      if (s + u < s1)
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+            a[u], *reinterpret_cast<const intx4 *>(codes + (s + u - s0) * kI8Step), acc, 0, 0, 0);
+  }
+  return acc;
+}
+
+// Dense: grid (column blocks of 16); up: grid (column blocks, pairs), the row
+// of a pair is its token's.
+template <int MODE, int KW, int B, int V>
+__global__ __launch_bounds__(64 * KW) void i8_direct_kernel(I8Args g, I8Direct d) {
+  __shared__ __attribute__((aligned(16))) uint8_t codes[KW][kDirectSteps * kI8Step];
+  __shared__ intx4 red[KW - 1][64];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  const int lane = tid % 64;
+  const int r = lane % 16;
+  const int grp = lane / 16;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int steps = g.kp / kI8Step;
+  const int per = (steps + KW - 1) / KW;
+  const int s0 = wave * per < steps ? wave * per : steps;
+  const int s1 = s0 + per < steps ? s0 + per : steps;
+  DirectRow<V> row;
+  row.request(d.x + (MODE == kI8Up ? static_cast<int64_t>(blockIdx.y / g.topk) * d.k : 0), d.k,
+              s0, s1, lane);
+  int64_t w0 = 0;
+  if constexpr (MODE == kI8Up) {
+    const int e = d.ids[blockIdx.y];
+    if (e < 0 || e >= d.n_experts) return;
+    w0 = static_cast<int64_t>(e) * g.n;
+  }
+  const int64_t nr = n0 + r < g.n ? n0 + r : g.n - 1;
+  const int8_t *wp = g.wq + (w0 + nr) * g.kp + 16 * grp;
+  intx4 a[B];
+  direct_load<B>(a, wp, s0, s1);
+  const RowScale rs = row.finish(codes[wave], lane);
+  intx4 acc = direct_sum<B>(a, wp, codes[wave] + 16 * grp, s0, s1);
+  if (wave > 0) red[wave - 1][lane] = acc;
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int w = 0; w < KW - 1; ++w) acc += red[w][lane];
+  if constexpr (MODE == kI8Dense) {
+    const intx4 block[1][1] = {{acc}};
+    const float scale[1] = {rs.scale};
+    store_any<1, 1>(g, block, 0, 1, n0, scale, lane);
+  } else if (r == 0) {
+    float sw[4];
+    load_sw(g, w0, n0 + 4 * grp, sw);
+    store_moe<MODE>(g, acc, blockIdx.y, n0 + 4 * grp, rs.scale, sw);
+  }
+}
+
+// The down product of single tokens with the weighted sum over their slots:
+// grid (column blocks of 16, tokens); waves 2 j and 2 j + 1 take the halves of
+// k of slot j.  Hidden rows are in pair order.  The sum runs in slot order with
+// the combine kernel's fused multiply-adds, so the bits are those of the
+// batched layer.
+constexpr int kDirectSlots = 8;
+
+template <int B, int V>
+__global__ __launch_bounds__(128 * kDirectSlots) void i8_direct_down_kernel(I8Args g, I8Direct d) {
+  __shared__ __attribute__((aligned(16))) uint8_t codes[2 * kDirectSlots][kDirectSteps * kI8Step];
+  __shared__ intx4 sums[2 * kDirectSlots][4];
+  __shared__ float scales[kDirectSlots];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  const int lane = tid % 64;
+  const int r = lane % 16;
+  const int grp = lane / 16;
+  const int slot = wave / 2;
+  const int64_t tok = blockIdx.y;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int steps = g.kp / kI8Step;
+  const int per = (steps + 1) / 2;
+  const int s0 = wave % 2 * per;
+  const int s1 = s0 + per < steps ? s0 + per : steps;
+  DirectRow<V> row;
+  row.request(d.x + (tok * g.topk + slot) * d.k, d.k, s0, s1, lane);
+  const int e = d.ids[tok * g.topk + slot];
+  if (e >= 0 && e < d.n_experts) {
+    const int64_t nr = n0 + r < g.n ? n0 + r : g.n - 1;
+    const int8_t *wp = g.wq + (e * g.n + nr) * g.kp + 16 * grp;
+    intx4 a[B];
+    direct_load<B>(a, wp, s0, s1);
+    const RowScale rs = row.finish(codes[wave], lane);
+    const intx4 acc = direct_sum<B>(a, wp, codes[wave] + 16 * grp, s0, s1);
+    if (r == 0) sums[wave][grp] = acc;
+    if (lane == 0) scales[slot] = rs.scale;  // the same from both halves
+  }
+  __syncthreads();
+  const int64_t n = n0 + tid;
+  if (tid >= 16 || n >= g.n) return;
+  float out = 0.f;
+  for (int j = 0; j < g.topk; ++j) {
+    const int ej = d.ids[tok * g.topk + j];
+    if (ej < 0 || ej >= d.n_experts) continue;
+    const int acc = sums[2 * j][tid / 4][tid % 4] + sums[2 * j + 1][tid / 4][tid % 4];
+    const float o = (static_cast<float>(acc) * scales[j]) * g.ws[ej * g.n + n];
+    out = __builtin_fmaf(d.gates[tok * g.topk + j], o, out);
+  }
+  static_cast<float *>(g.y)[tok * g.n + n] = out;
 }
 
 // A wave's MS x NS sub-tiles to memory through LDS.  Straight from the product's
@@ -1069,6 +1280,97 @@ hipError_t launch_int8_cache(const uint8_t *packed, int64_t n, int64_t k, uint32
   const int64_t grid = n < 65536 ? n : 65536;
   hipLaunchKernelGGL(int8_cache_kernel, dim3(static_cast<unsigned>(grid)), dim3(kQThreads), 0, s,
                      packed, n, k / 32, int8_padded_k(k), sign_bits, codebook(), codes, scales);
+  return hipGetLastError();
+}
+
+namespace {
+
+int direct_steps(int64_t k, int waves) {
+  const int64_t steps = int8_padded_k(k) / kI8Step;
+  return static_cast<int>((steps + waves - 1) / waves);
+}
+
+template <int MODE, int KW, int B>
+hipError_t launch_direct(const I8Args &g, const I8Direct &d, dim3 grid, hipStream_t s) {
+  if (d.k <= 64 * 8 * 6)
+    hipLaunchKernelGGL((i8_direct_kernel<MODE, KW, B, 6>), grid, dim3(64 * KW), 0, s, g, d);
+  else
+    hipLaunchKernelGGL((i8_direct_kernel<MODE, KW, B, kDirectVecs>), grid, dim3(64 * KW), 0, s, g,
+                       d);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool int8_direct_fits(int64_t m, int64_t k) {
+  return m == 1 && k <= 64 * 8 * kDirectVecs && direct_steps(k, 8) <= kDirectSteps;
+}
+
+hipError_t launch_linear_int8_direct(const uint16_t *x, int64_t m, int64_t k, const int8_t *wq,
+                                     const float *ws, int64_t n, const Tail &tail, void *y,
+                                     hipStream_t s) {
+  if (!int8_direct_fits(m, k)) return hipErrorInvalidValue;
+  I8Args g{};
+  g.wq = wq;
+  g.ws = ws;
+  g.y = y;
+  g.tail = tail;
+  g.m = m;
+  g.n = n;
+  g.kp = static_cast<int32_t>(int8_padded_k(k));
+  const size_t quad = tail.bf16 ? 8 : 16;
+  g.vec = n % 4 == 0 && reinterpret_cast<uintptr_t>(y) % quad == 0 &&
+          reinterpret_cast<uintptr_t>(tail.residual) % quad == 0;
+  I8Direct d{};
+  d.x = x;
+  d.k = static_cast<int32_t>(k);
+  const dim3 grid(static_cast<unsigned>((n + 15) / 16));
+  if (direct_steps(k, 8) <= 6) return launch_direct<kI8Dense, 8, 6>(g, d, grid, s);
+  return launch_direct<kI8Dense, 8, 8>(g, d, grid, s);
+}
+
+// Up to 12 pairs (two tokens of six slots), and the row and step limits of the
+// kernels.  128 experts of 1856 x 2688, top-6: one token 25 us against 33 for
+// the batched steps, two 39 against 44, four 65 against 62 (the batched steps
+// read an expert that two tokens share once).
+bool int8_moe_direct_fits(int64_t t, int32_t topk, int64_t n1, int64_t k) {
+  return t * topk <= 12 && topk <= kDirectSlots && k <= 64 * 8 * kDirectVecs &&
+         direct_steps(k, 4) <= kDirectSteps && direct_steps(n1, 2) <= kDirectSteps;
+}
+
+hipError_t launch_moe_int8_direct(const uint16_t *x, int64_t t, int64_t k, const int32_t *ids,
+                                  const float *gates, int32_t topk, int32_t n_experts,
+                                  const int8_t *w1, const float *s1, int64_t n1, const int8_t *w2,
+                                  const float *s2, uint16_t *h, float *out, hipStream_t s) {
+  if (!int8_moe_direct_fits(t, topk, n1, k)) return hipErrorInvalidValue;
+  I8Args g{};
+  g.wq = w1;
+  g.ws = s1;
+  g.y = h;
+  g.n = n1;
+  g.kp = static_cast<int32_t>(int8_padded_k(k));
+  g.topk = topk;
+  I8Direct d{};
+  d.x = x;
+  d.k = static_cast<int32_t>(k);
+  d.ids = ids;
+  d.gates = gates;
+  d.n_experts = n_experts;
+  const dim3 grid1(static_cast<unsigned>((n1 + 15) / 16), static_cast<unsigned>(t * topk));
+  const hipError_t e = direct_steps(k, 4) <= 8 ? launch_direct<kI8Up, 4, 8>(g, d, grid1, s)
+                                               : launch_direct<kI8Up, 4, 11>(g, d, grid1, s);
+  if (e != hipSuccess) return e;
+  g.wq = w2;
+  g.ws = s2;
+  g.y = out;
+  g.n = k;
+  g.kp = static_cast<int32_t>(int8_padded_k(n1));
+  d.x = h;
+  d.k = static_cast<int32_t>(n1);
+  const dim3 grid2(static_cast<unsigned>((k + 15) / 16), static_cast<unsigned>(t));
+  // two halves of at most 16 steps: rows of at most 2048 values
+  hipLaunchKernelGGL((i8_direct_down_kernel<kDirectSteps, 4>), grid2,
+                     dim3(static_cast<unsigned>(128 * topk)), 0, s, g, d);
   return hipGetLastError();
 }
 

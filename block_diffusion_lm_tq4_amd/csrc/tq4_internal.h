@@ -337,6 +337,19 @@ hipError_t launch_int8_cache(const uint8_t *packed, int64_t n, int64_t k, uint32
 hipError_t launch_linear_int8(const int8_t *xq, const float *xs, int64_t m, int64_t k,
                               const int8_t *wq, const float *ws, int64_t n, const Tail &tail,
                               void *y, hipStream_t s);
+// The same from bf16 rows in one launch, for the few rows and the k that
+// int8_direct_fits takes; bit-equal.
+bool int8_direct_fits(int64_t m, int64_t k);
+hipError_t launch_linear_int8_direct(const uint16_t *x, int64_t m, int64_t k, const int8_t *wq,
+                                     const float *ws, int64_t n, const Tail &tail, void *y,
+                                     hipStream_t s);
+// The MoE layer of a few tokens in two launches, without bucketing (h: bf16
+// [t * topk][n1], in pair order); bit-equal to the batched steps.
+bool int8_moe_direct_fits(int64_t t, int32_t topk, int64_t n1, int64_t k);
+hipError_t launch_moe_int8_direct(const uint16_t *x, int64_t t, int64_t k, const int32_t *ids,
+                                  const float *gates, int32_t topk, int32_t n_experts,
+                                  const int8_t *w1, const float *s1, int64_t n1, const int8_t *w2,
+                                  const float *s2, uint16_t *h, float *out, hipStream_t s);
 // Grouped products over stacked int8 experts (expert e's rows at e * n of the
 // [E * n, k] cache).  mode 0 (up): rows gathered as perm[row] / topk; out is
 // bf16 [pairs][n], relu(u)^2.  a_rows: rows of aq.  mode 1 (down): bucket rows; out is fp32

@@ -523,15 +523,22 @@ def _call(fn: str, dev: torch.device, *args) -> None:
 
 
 def _arg_on(t: torch.Tensor, name: str, dtype, dev: torch.device) -> None:
-    _cuda_contig(t, name, dtype)
-    _require(t.device == dev, f"{name} must be on {dev}")
+    """t must be a contiguous tensor of this type on dev (a device)."""
+    if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _cuda_contig(t, name, dtype)
+        _require(t.device == dev, f"{name} must be on {dev}")
 
 
-def _scratch(workspace: torch.Tensor | None, nbytes: int, dev: torch.device) -> torch.Tensor:
+def _scratch(workspace: torch.Tensor | None, nbytes: int,
+             dev: torch.device) -> tuple[torch.Tensor | None, int | None, int]:
+    """(tensor to hold on to, pointer, size) of the caller's or of new scratch memory."""
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _arg_on(workspace, "workspace", torch.uint8, dev)
-    return workspace
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        _arg_on(workspace, "workspace", torch.uint8, dev)
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def int8_padded_k(k: int) -> int:
@@ -626,9 +633,8 @@ def _linear_int8(fn, x, cache, n, tail, out, workspace, ydtype):
     else:
         _arg_on(out, "out", ydtype, dev)
         _require(tuple(out.shape) == (m, n), "out must be [m, n]")
-    workspace = _scratch(workspace, linear_int8_workspace_size(m, k, n), dev)
-    _call(fn, dev, x.data_ptr(), m, k, cache.data_ptr(), n, *ptrs, out.data_ptr(),
-          workspace.data_ptr(), workspace.numel())
+    held, ws, ws_size = _scratch(workspace, lib().tq4_linear_int8_workspace_size(m, k, n), dev)
+    _call(fn, dev, x.data_ptr(), m, k, cache.data_ptr(), n, *ptrs, out.data_ptr(), ws, ws_size)
     return out
 
 
@@ -712,11 +718,11 @@ def moe_grouped_int8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tens
     else:
         _arg_on(out, "out", torch.float32, dev)
         _require(tuple(out.shape) == (t, k), "out must be [t, k]")
-    workspace = _scratch(workspace, moe_grouped_int8_workspace_size(t, topk, n_experts, n1, k),
-                         dev)
+    held, ws, ws_size = _scratch(
+        workspace, moe_grouped_int8_workspace_size(t, topk, n_experts, n1, k), dev)
     _call("tq4_moe_grouped_int8", dev, x.data_ptr(), t, k, topk_ids.data_ptr(),
           topk_w.data_ptr(), topk, n_experts, w1_cache.data_ptr(), n1, w2_cache.data_ptr(),
-          out.data_ptr(), workspace.data_ptr(), workspace.numel())
+          out.data_ptr(), ws, ws_size)
     return out
 
 

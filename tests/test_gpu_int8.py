@@ -267,7 +267,8 @@ def test_linear_refusals(dev):
     with pytest.raises(TQ4Error, match="ALIGN"):
         _ops().linear_int8(x, torch.zeros(2000, dtype=torch.uint8, device=dev)[4:], 8)
     with pytest.raises(TQ4Error, match="WORKSPACE"):
-        _ops().linear_int8(x, cache, 8, workspace=torch.empty(8, dtype=torch.uint8, device=dev))
+        _ops().linear_int8(torch.zeros(40, 64, dtype=torch.bfloat16, device=dev), cache, 8,
+                           workspace=torch.empty(8, dtype=torch.uint8, device=dev))
 
 
 # ---- the MoE layer ---------------------------------------------------------
