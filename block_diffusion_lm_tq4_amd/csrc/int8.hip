@@ -446,6 +446,14 @@ __device__ inline void store_any(const I8Args &g, const intx4 (&acc)[MS][NS], in
 
 // Scales of columns n .. n + 3 (row w0 + n of the stacked weights).
 __device__ inline void load_sw(const I8Args &g, int64_t w0, int64_t n, float (&sw)[4]) {
+  if (n + 4 <= g.n && (w0 + n) % 4 == 0) {
+    const float4 d = *reinterpret_cast<const float4 *>(g.ws + w0 + n);
+    sw[0] = d.x;
+    sw[1] = d.y;
+    sw[2] = d.z;
+    sw[3] = d.w;
+    return;
+  }
 #pragma unroll
   for (int v = 0; v < 4; ++v) sw[v] = n + v < g.n ? g.ws[w0 + n + v] : 0.f;
 }
@@ -787,8 +795,8 @@ typedef uint32_t uintx2 __attribute__((ext_vector_type(2)));
 
 template <int MODE, int MS, int NS, int WM, bool BF16, bool VEC>
 __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], uint8_t *lds,
-                                  int64_t m0, int rows, int64_t n0, int64_t w0,
-                                  const float (&sx)[MS], int lane) {
+                                  int64_t m0, int rows, int64_t n0, const float (&sx)[MS],
+                                  const float (&sw)[NS][4], int lane) {
 #pragma clang fp contract(off)
   constexpr int kCols = 16 * NS;
   constexpr int kStride = kCols + 4;
@@ -798,14 +806,6 @@ __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], u
   const int grp = lane / 16;
   const bool has_bias = MODE == kI8Dense && g.tail.bias != nullptr;
   const bool has_res = MODE == kI8Dense && g.tail.residual != nullptr;
-  float sw[NS][4];
-#pragma unroll
-  for (int j = 0; j < NS; ++j)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t n = n0 + 16 * j + 4 * grp + v;
-      sw[j][v] = n < g.n ? g.ws[w0 + n] : 0.f;
-    }
   // this lane's columns in the row image are the same for every group of rows
   // when a row is a divisor of 64 * E outputs, which it is for NS = 1, 2, 4
   // (and 8 with E = 4 loops twice over half-waves' rows)
@@ -941,11 +941,13 @@ __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], u
 // S - 1 steps ahead, with exact load-count waits and one barrier per step.
 //
 // LDS image of a stage: 1 KB pieces of 1024 / KB rows; a row's 16-byte slots
-// are stored at slot ^ key(row), key = (row / 4) % 4 for 64-byte rows and
-// (row / 2) % 8 for 128-byte rows, so the 16 rows that a fragment read visits
-// at one slot fall on all 64 banks.  Rows past the tile's end read zeros
-// (dense; the buffer range ends there) or the tile's first row (MoE) and are
-// not stored.
+// are stored at slot ^ key(row).  A 16-byte read takes the wave in phases of 16
+// lanes, which are not consecutive (0-3, 12-15, 20-23, 24-27 make the first):
+// of lane r + 16 g reading row r, a phase holds rows 0-3 and 12-15 at one slot
+// and 4-11 at another.  key = (row / 2) % 8 for 128-byte rows and 0, 2, 3, 1 for
+// row / 4 = 0 .. 3 of 64-byte rows put the 16 lanes of every phase on all 64
+// banks.  Rows past the tile's end read zeros (dense; the buffer range ends
+// there) or the tile's first row (MoE) and are not stored.
 template <int MODE, int WM, int WN, int MS, int NS, int KB, int S, int OCC, bool PP>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
   constexpr int W = WM * WN;
@@ -1008,9 +1010,12 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
   // A piece's lane l fills row l / kSlots at stored slot l % kSlots; the key of
   // a row depends on row % 16, so the pieces of 8 rows alternate between two.
   const int prow = lane / kSlots;
-  auto slot_of = [&](int row) __attribute__((always_inline)) {
-    return (lane % kSlots) ^ (KB == 64 ? (row >> 2) & 3 : (row >> 1) & 7);
+  auto key_of = [](int row) __attribute__((always_inline)) {
+    if constexpr (KB == 64) return ((row >> 1) & 2) ^ ((row >> 3) & 1) * 3;
+    return (row >> 1) & 7;
   };
+  auto slot_of = [&](int row)
+      __attribute__((always_inline)) { return (lane % kSlots) ^ key_of(row); };
   const int64_t a_base = MODE == kI8Dense ? m_base : 0;
   const int64_t a_rows = MODE == kI8Dense ? rows : g.a_rows;
   const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
@@ -1055,6 +1060,19 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
           0);
   };
 
+  // The up products' row scales are two loads away (through the bucket order),
+  // so they are fetched before the k loop.
+  float sx[MS];
+  auto load_sx = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MS; ++i) {
+      const int row = 16 * (WM * i + wm) + r;
+      const int64_t b = m_base + (row < rows ? row : 0);
+      sx[i] = g.xs[MODE == kI8Up ? g.perm[b] / g.topk : b];
+    }
+  };
+  if constexpr (MODE == kI8Up) load_sx();
+
   intx4 acc[MS][NS];
 #pragma unroll
   for (int i = 0; i < MS; ++i)
@@ -1062,7 +1080,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
     for (int j = 0; j < NS; ++j) acc[i][j] = intx4{0, 0, 0, 0};
 
   // fragment addresses: row 16 * x + r, whose key depends on r alone
-  const int key = KB == 64 ? (r >> 2) & 3 : (r >> 1) & 7;
+  const int key = key_of(r);
   const int a_frag = (16 * wm + r) * KB;
   const int w_frag = kWBase + (wn * (16 * NS) + r) * KB;
   // A wave's sub-tile i holds rows 16 (WM i + wm) ..., so that the rows of a
@@ -1149,33 +1167,34 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
     }
   }
   static_assert(W * tile_store_bytes<NS>() <= S * kStage, "the stages hold the store buffers");
+  // the scales arrive while the last steps drain
+  if constexpr (MODE != kI8Up) load_sx();
+  const int64_t m0 = m_base + 16 * wm;
+  const int64_t n0 = n_base + wn * (16 * NS);
+  float sw[NS][4];
+#pragma unroll
+  for (int j = 0; j < NS; ++j) {
+    const int64_t n = n0 + 16 * j + 4 * grp;
+    load_sw(g, w0, n, sw[j]);
+  }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // the padding steps' loads
   __builtin_amdgcn_s_waitcnt(0xC07F);  // the last reads of the stages
   __syncthreads();                     // for every wave: the stages become store buffers
 
-  float sx[MS];
-#pragma unroll
-  for (int i = 0; i < MS; ++i) {
-    const int row = 16 * (WM * i + wm) + r;
-    const int64_t b = m_base + (row < rows ? row : 0);
-    sx[i] = g.xs[MODE == kI8Up ? g.perm[b] / g.topk : b];
-  }
   uint8_t *lds = smem + wave * tile_store_bytes<NS>();
-  const int64_t m0 = m_base + 16 * wm;
-  const int64_t n0 = n_base + wn * (16 * NS);
   rows -= 16 * wm;
   if constexpr (MODE != kI8Dense) {
-    store_rows<MODE, MS, NS, WM, MODE == kI8Up, true>(g, acc, lds, m0, rows, n0, w0, sx, lane);
+    store_rows<MODE, MS, NS, WM, MODE == kI8Up, true>(g, acc, lds, m0, rows, n0, sx, sw, lane);
   } else if (g.vec) {
     if (g.tail.bf16)
-      store_rows<MODE, MS, NS, WM, true, true>(g, acc, lds, m0, rows, n0, 0, sx, lane);
+      store_rows<MODE, MS, NS, WM, true, true>(g, acc, lds, m0, rows, n0, sx, sw, lane);
     else
-      store_rows<MODE, MS, NS, WM, false, true>(g, acc, lds, m0, rows, n0, 0, sx, lane);
+      store_rows<MODE, MS, NS, WM, false, true>(g, acc, lds, m0, rows, n0, sx, sw, lane);
   } else {
     if (g.tail.bf16)
-      store_rows<MODE, MS, NS, WM, true, false>(g, acc, lds, m0, rows, n0, 0, sx, lane);
+      store_rows<MODE, MS, NS, WM, true, false>(g, acc, lds, m0, rows, n0, sx, sw, lane);
     else
-      store_rows<MODE, MS, NS, WM, false, false>(g, acc, lds, m0, rows, n0, 0, sx, lane);
+      store_rows<MODE, MS, NS, WM, false, false>(g, acc, lds, m0, rows, n0, sx, sw, lane);
   }
 }
 
