@@ -284,8 +284,11 @@ enum { kI8Dense = 0, kI8Up = 1, kI8Down = 2 };
 typedef __attribute__((address_space(3))) void lds_void;
 constexpr int kI8BufferFlags = 0x00020000;
 
-__device__ inline uint16_t bf16_bits(float v) {
-  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+// Two values rounded to bf16 (ties to even), a in the low half.
+__device__ inline uint32_t bf16_pair(float a, float b) {
+  typedef float pair __attribute__((ext_vector_type(2)));
+  typedef __bf16 out __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((pair{a, b}), out));
 }
 
 // The hidden value by its definition: u in fp64, relu(u)^2 rounded to fp32
@@ -297,31 +300,38 @@ __device__ inline float hidden_f64(int acc, float sx, float sw) {
 }
 
 // The same for four sums of one row, in fp32 where that decides it.  With both
-// scales zero or in [2^-30, 2^16] (`tame`) nothing leaves fp32's normal range:
-// u = acc * (sx * sw) carries at most three roundings and its square seven, 7 *
-// 2^-24 relative, i.e. at most 7 fp32 steps, so the bf16 rounding is settled
-// unless the low 16 bits are within 8 of the tie.  About one value in 4000 is
-// not, and its quad takes fp64.  (Written with a test for each value, this was
-// 100 of the up product's 250 us at 4096 tokens.)
+// scales zero or in [2^-30, 2^16] (`tame`, of all the wave's) nothing leaves
+// fp32's normal range: u = acc * (sx * sw) carries at most three roundings and
+// its square seven, 7 * 2^-24 relative, i.e. at most 7 fp32 steps, so the bf16
+// rounding is settled unless the low 16 bits are within 8 of the tie.  About one
+// value in 4000 is not, and its wave's quads take fp64.  The test takes 1.5
+// instructions a value, on halves packed in pairs, and one branch a quad: at 4096
+// tokens the up product is bound by what its epilogue issues as much as by what
+// it stores (a compare and a flag for each value: 6 us of 197 more, a
+// branch for each: 100 more).
 __device__ inline bool tame_scale(float s) {
   return s == 0.f || (s >= 0x1p-30f && s <= 0x1p+16f);
 }
 
 __device__ inline uint2 hidden_quad(intx4 acc, float sx, const float (&sw)[4], bool tame) {
   float h[4];
-  bool slow = !tame;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const float u = static_cast<float>(acc[v] > 0 ? acc[v] : 0) * (sx * sw[v]);
     h[v] = u * u;
-    slow |= ((__float_as_uint(h[v]) - (0x8000u - 8u)) & 0xFFFFu) <= 16u;
   }
-  if (__builtin_expect(__any(slow), 0)) {
+  // the low halves, moved so that 8 below the tie is 0
+  auto low = [](float a, float b) {
+    const uint32_t d = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x05040100u);
+    return __builtin_bit_cast(ushortx2, d) + ushortx2{0x8008, 0x8008};
+  };
+  const ushortx2 near = __builtin_elementwise_min(low(h[0], h[1]), low(h[2], h[3]));
+  const uint16_t nearest = near[0] < near[1] ? near[0] : near[1];
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(nearest <= (tame ? 16 : 0xFFFF)) != 0, 0)) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) h[v] = hidden_f64(acc[v], sx, sw[v]);
   }
-  return make_uint2(bf16_bits(h[0]) | static_cast<uint32_t>(bf16_bits(h[1])) << 16,
-                    bf16_bits(h[2]) | static_cast<uint32_t>(bf16_bits(h[3])) << 16);
+  return make_uint2(bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3]));
 }
 
 // One row's four consecutive outputs n .. n + 3 of the MoE products (n % 32
@@ -331,8 +341,9 @@ __device__ inline void store_moe(const I8Args &g, intx4 acc, int64_t row, int64_
                                  const float (&sw)[4]) {
   if (n >= g.n) return;
   if constexpr (MODE == kI8Up) {
-    const bool tame = tame_scale(sx) && tame_scale(sw[0]) && tame_scale(sw[1]) &&
-                      tame_scale(sw[2]) && tame_scale(sw[3]);
+    const bool own = tame_scale(sx) && tame_scale(sw[0]) && tame_scale(sw[1]) &&
+                     tame_scale(sw[2]) && tame_scale(sw[3]);
+    const bool tame = __builtin_amdgcn_ballot_w64(!own) == 0;
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.y) + row * g.n + n) =
         hidden_quad(acc, sx, sw, tame);
   } else {
@@ -376,8 +387,7 @@ __device__ inline void store_dense(const I8Args &g, int64_t at, int left, const 
   float *y = static_cast<float *>(g.y);
   if constexpr (VEC && BF16) {
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.y) + at) =
-        make_uint2(bf16_bits(p[0]) | static_cast<uint32_t>(bf16_bits(p[1])) << 16,
-                   bf16_bits(p[2]) | static_cast<uint32_t>(bf16_bits(p[3])) << 16);
+        make_uint2(bf16_pair(p[0], p[1]), bf16_pair(p[2], p[3]));
   } else if constexpr (VEC) {
     *reinterpret_cast<float4 *>(y + at) = make_float4(p[0], p[1], p[2], p[3]);
   } else {
@@ -848,6 +858,7 @@ __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], u
       for (int v = 0; v < 4; ++v) tame = tame && tame_scale(sw[j][v]);
 #pragma unroll
     for (int i = 0; i < MS; ++i) tame = tame && tame_scale(sx[i]);
+    tame = __builtin_amdgcn_ballot_w64(!tame) == 0;
     constexpr int kRowBytes = 2 * kCols + 16;
     constexpr int kReads = 16 * kCols / 512;  // of 64 lanes x 8 outputs
     static_assert(kReads >= 1, "two or more column sub-tiles");
@@ -862,12 +873,13 @@ __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], u
 #pragma unroll
       for (int q = 0; q < kReads; ++q) {
         const int f = 512 * q + 8 * lane;
-        const uint4 d = *reinterpret_cast<const uint4 *>(buf + (f / kCols) * kRowBytes +
+        const intx4 d = *reinterpret_cast<const intx4 *>(buf + (f / kCols) * kRowBytes +
                                                          2 * (f % kCols));
         const int row = 16 * WM * i + f / kCols;
         const int64_t n = n0 + f % kCols;
         if (row < rows && n < g.n)  // n % 32 == 0 columns in all
-          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(g.y) + (m0 + row) * g.n + n) = d;
+          __builtin_nontemporal_store(
+              d, reinterpret_cast<intx4 *>(static_cast<uint16_t *>(g.y) + (m0 + row) * g.n + n));
       }
     }
     return;
@@ -913,20 +925,13 @@ __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], u
       if (row >= rows || n >= g.n) continue;
       const int64_t at = (m0 + row) * g.n + n;
       if constexpr (VEC && BF16) {
-        const uintx2 d = {bf16_bits(val[q][0]) | static_cast<uint32_t>(bf16_bits(val[q][1])) << 16,
-                          bf16_bits(val[q][2]) | static_cast<uint32_t>(bf16_bits(val[q][3])) << 16};
+        const uintx2 d = {bf16_pair(val[q][0], val[q][1]), bf16_pair(val[q][2], val[q][3])};
         uintx2 *dst = reinterpret_cast<uintx2 *>(static_cast<uint16_t *>(g.y) + at);
-        if constexpr (MODE != kI8Up)
-          __builtin_nontemporal_store(d, dst);
-        else
-          *dst = d;
+        __builtin_nontemporal_store(d, dst);
       } else if constexpr (VEC) {
         const floatx4 d = {val[q][0], val[q][1], val[q][2], val[q][3]};
         floatx4 *dst = reinterpret_cast<floatx4 *>(static_cast<float *>(g.y) + at);
-        if constexpr (MODE != kI8Up)
-          __builtin_nontemporal_store(d, dst);
-        else
-          *dst = d;
+        __builtin_nontemporal_store(d, dst);
       } else {
         tail_store_as<BF16>(static_cast<float *>(g.y), at, val[q][0]);
       }
@@ -1060,18 +1065,20 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
           0);
   };
 
-  // The up products' row scales are two loads away (through the bucket order),
-  // so they are fetched before the k loop.
-  float sx[MS];
-  auto load_sx = [&]() __attribute__((always_inline)) {
+  // The scales that the epilogue applies, fetched before the k loop: behind it
+  // every wave of the tile would stand for them (5 us of the up product's 197 at
+  // 4096 tokens).
+  const int64_t m0 = m_base + 16 * wm;
+  const int64_t n0 = n_base + wn * (16 * NS);
+  float sx[MS], sw[NS][4];
 #pragma unroll
-    for (int i = 0; i < MS; ++i) {
-      const int row = 16 * (WM * i + wm) + r;
-      const int64_t b = m_base + (row < rows ? row : 0);
-      sx[i] = g.xs[MODE == kI8Up ? g.perm[b] / g.topk : b];
-    }
-  };
-  if constexpr (MODE == kI8Up) load_sx();
+  for (int i = 0; i < MS; ++i) {
+    const int row = 16 * (WM * i + wm) + r;
+    const int64_t b = m_base + (row < rows ? row : 0);
+    sx[i] = g.xs[MODE == kI8Up ? g.perm[b] / g.topk : b];
+  }
+#pragma unroll
+  for (int j = 0; j < NS; ++j) load_sw(g, w0, n0 + 16 * j + 4 * grp, sw[j]);
 
   intx4 acc[MS][NS];
 #pragma unroll
@@ -1167,16 +1174,6 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
     }
   }
   static_assert(W * tile_store_bytes<NS>() <= S * kStage, "the stages hold the store buffers");
-  // the scales arrive while the last steps drain
-  if constexpr (MODE != kI8Up) load_sx();
-  const int64_t m0 = m_base + 16 * wm;
-  const int64_t n0 = n_base + wn * (16 * NS);
-  float sw[NS][4];
-#pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    const int64_t n = n0 + 16 * j + 4 * grp;
-    load_sw(g, w0, n, sw[j]);
-  }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // the padding steps' loads
   __builtin_amdgcn_s_waitcnt(0xC07F);  // the last reads of the stages
   __syncthreads();                     // for every wave: the stages become store buffers
