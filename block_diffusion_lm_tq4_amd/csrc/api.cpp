@@ -872,10 +872,9 @@ int tq4_moe_grouped_int8(const uint16_t *x_bf16, int64_t t, int64_t k, const int
         reinterpret_cast<const int8_t *>(w1_cache), int8_scales(w1_cache, e64 * n1, k), n1,
         reinterpret_cast<const int8_t *>(w2_cache), int8_scales(w2_cache, e64 * k, n1), h, out,
         s));
-  hipError_t e = tq4::launch_act_int8(x_bf16, t, k, xq, xs, s);
-  if (e == hipSuccess)
-    e = tq4::launch_route(topk_ids, pairs, topk, n_experts, counts, offsets, perm, inv, tiles,
-                          meta, l.tile_rows, nullptr, s);
+  hipError_t e =
+      tq4::launch_moe_int8_prepare(x_bf16, t, k, topk_ids, topk, n_experts, counts, offsets, perm,
+                                   inv, tiles, meta, l.tile_rows, xq, xs, s);
   if (e == hipSuccess)
     e = tq4::launch_moe_int8(0, l.tile_rows, xq, xs, t, k, perm, topk,
                              reinterpret_cast<const int8_t *>(w1_cache),

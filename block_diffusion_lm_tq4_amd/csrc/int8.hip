@@ -35,6 +35,10 @@ typedef int intx4 __attribute__((ext_vector_type(4)));
 
 constexpr int kI8Step = 64;
 
+constexpr int kRouteThreads = 1024;
+constexpr int kRouteWaves = kRouteThreads / 64;
+#include "moe_route.h"
+
 // A wave's LDS writes before its later reads (nothing but the compiler could
 // change their order).
 __device__ inline void wave_lds_fence() {
@@ -132,10 +136,51 @@ __device__ inline ushortx2 top_of(uint4 d) {
 }
 __device__ inline uint32_t top_of(ushortx2 t) { return t[0] > t[1] ? t[0] : t[1]; }
 
-// bf16 rows, T threads each (64: a wave per row, four rows per workgroup, no
-// barrier; 256: the workgroup).  A row of up to T * 8 * V values stays in
-// registers between the maximum and the codes; longer ones are read twice.
-// HBM-bound: 3 bytes per value.
+// One bf16 row by T threads (thread tid of them); `red` is for T > 64, which all
+// threads of the workgroup enter together.  A row of up to T * 8 * V values
+// stays in registers between the maximum and the codes; longer ones are read
+// twice.
+template <int T, int V>
+__device__ inline void act_row(const uint4 *xr, int32_t k, int32_t kp, int tid, uint32_t *red,
+                               uint2 *qr, float *scale) {
+  const int n_vec = k / 8;    // k is a multiple of 32
+  const int n_out = kp / 8;
+  uint4 d[V];
+  ushortx2 tops = {0, 0};
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int at = tid + T * i;
+    d[i] = at < n_vec ? xr[at] : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) tops = __builtin_elementwise_max(tops, top_of(d[i]));
+  for (int at = tid + T * V; at < n_vec; at += T)
+    tops = __builtin_elementwise_max(tops, top_of(xr[at]));
+  uint32_t top = top_of(tops);
+  if constexpr (T == 64) {
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const uint32_t o = __shfl_xor(top, s);
+      top = top > o ? top : o;
+    }
+  } else {
+    top = group_max(top, red);
+    __syncthreads();
+  }
+  const RowScale rs(top);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int at = tid + T * i;
+    if (at < n_out)
+      qr[at] = rs.live ? codes_of(d[i], rs) : make_uint2(0u, 0u);
+  }
+  for (int at = tid + T * V; at < n_out; at += T)
+    qr[at] = rs.live && at < n_vec ? codes_of(xr[at], rs) : make_uint2(0u, 0u);
+  if (tid == 0) *scale = rs.scale;
+}
+
+// Rows of a matrix, T threads each (64: a wave per row, four rows per workgroup,
+// no barrier; 256: the workgroup).  HBM-bound: 3 bytes per value.
 template <int T, int V>
 __global__ __launch_bounds__(kQThreads) void act_int8_kernel(const uint16_t *__restrict__ x,
                                                              int64_t m, int32_t k, int32_t kp,
@@ -143,46 +188,34 @@ __global__ __launch_bounds__(kQThreads) void act_int8_kernel(const uint16_t *__r
                                                              float *__restrict__ scales) {
   __shared__ uint32_t red[kQThreads / 64];
   constexpr int kRows = kQThreads / T;
-  const int tid = threadIdx.x % T;
-  const int n_vec = k / 8;    // k is a multiple of 32
-  const int n_out = kp / 8;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T; row < m;
-       row += static_cast<int64_t>(gridDim.x) * kRows) {
-    const uint4 *xr = reinterpret_cast<const uint4 *>(x + row * k);
-    uint2 *qr = reinterpret_cast<uint2 *>(codes + row * kp);
-    uint4 d[V];
-    ushortx2 tops = {0, 0};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int at = tid + T * i;
-      d[i] = at < n_vec ? xr[at] : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) tops = __builtin_elementwise_max(tops, top_of(d[i]));
-    for (int at = tid + T * V; at < n_vec; at += T)
-      tops = __builtin_elementwise_max(tops, top_of(xr[at]));
-    uint32_t top = top_of(tops);
-    if constexpr (T == 64) {
-#pragma unroll
-      for (int s = 1; s < 64; s <<= 1) {
-        const uint32_t o = __shfl_xor(top, s);
-        top = top > o ? top : o;
-      }
-    } else {
-      top = group_max(top, red);
-      __syncthreads();
-    }
-    const RowScale rs(top);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int at = tid + T * i;
-      if (at < n_out)
-        qr[at] = rs.live ? codes_of(d[i], rs) : make_uint2(0u, 0u);
-    }
-    for (int at = tid + T * V; at < n_out; at += T)
-      qr[at] = rs.live && at < n_vec ? codes_of(xr[at], rs) : make_uint2(0u, 0u);
-    if (tid == 0) scales[row] = rs.scale;
+       row += static_cast<int64_t>(gridDim.x) * kRows)
+    act_row<T, V>(reinterpret_cast<const uint4 *>(x + row * k), k, kp, threadIdx.x % T, red,
+                  reinterpret_cast<uint2 *>(codes + row * kp), scales + row);
+}
+
+// The MoE layer's first launch: workgroup 0 buckets the pairs, the others
+// quantize the tokens, a wave per row.  Neither needs the other's result, and
+// the bucketing is one workgroup's chain of latencies (7 us for 16 tokens, 12
+// for 1024) in which the rest of the device is free.
+__global__ __launch_bounds__(kRouteThreads) void i8_route_act_kernel(
+    const int32_t *ids, int64_t pairs, int32_t n_experts, int32_t *counts, int32_t *offsets,
+    int32_t *perm, int32_t *inv, MoETile *tiles, int32_t *n_tiles, int32_t tile_rows,
+    const uint16_t *__restrict__ x, int64_t t, int32_t k, int32_t kp, int8_t *__restrict__ codes,
+    float *__restrict__ scales) {
+  __shared__ int32_t hist[kRouteWaves][kMaxExperts];
+  __shared__ int32_t base[kMaxExperts + 1];
+  __shared__ int32_t tile_base[kMaxExperts + 1];
+  if (blockIdx.x > 0) {
+    const int64_t row =
+        static_cast<int64_t>(blockIdx.x - 1) * kRouteWaves + threadIdx.x / 64;
+    if (row < t)
+      act_row<64, 8>(reinterpret_cast<const uint4 *>(x + row * k), k, kp, threadIdx.x % 64,
+                     nullptr, reinterpret_cast<uint2 *>(codes + row * kp), scales + row);
+    return;
   }
+  bucket_group<kRouteWaves>(hist, base, tile_base, ids, pairs, n_experts, counts, offsets, perm,
+                            inv, tiles, n_tiles, tile_rows, nullptr);
 }
 
 // Packed TQ4_1S rows, one workgroup per row, in fp64: the butterfly's sums v
@@ -791,8 +824,9 @@ __global__ __launch_bounds__(128 * kDirectSlots) void i8_direct_down_kernel(I8Ar
 // half a cache line each; instead 16 rows at a time go to a wave's own LDS
 // buffer (two in turn, rows 16 bytes longer than their data, so that neither
 // the writes nor the reads share banks) and come back as whole row segments
-// of 16 * NS outputs.  Stores are non-temporal in the dense mode, whose
-// output is larger than the caches it would push the operands out of.
+// of 16 * NS outputs.  Stores are non-temporal: nothing reads the output before
+// the operands that it would push out of the caches are needed (4096 x 2688 x
+// 8192: 107 -> 96 us, the up product of 1024 tokens 149 -> 142).
 // Residual values of the next 16 rows are loaded before the stores of these,
 // since a wait for a load is also one for every store before it.
 template <int NS>
@@ -1287,6 +1321,30 @@ hipError_t launch_act_int8(const uint16_t *x, int64_t m, int64_t k, int8_t *code
   else
     hipLaunchKernelGGL((act_int8_kernel<256, 4>), grid, dim3(kQThreads), 0, s, x, m, k32, kp,
                        codes, scales);
+  return hipGetLastError();
+}
+
+// In one launch where one workgroup buckets and a row stays in a wave's
+// registers (6.7 us for 16 tokens x 2688, 10.3 for 1024; in two launches 4.4 +
+// 6.9 and 6.5 + 10.5), in two or four otherwise.
+hipError_t launch_moe_int8_prepare(const uint16_t *x, int64_t t, int64_t k, const int32_t *ids,
+                                   int32_t topk, int32_t n_experts, int32_t *counts,
+                                   int32_t *offsets, int32_t *perm, int32_t *inv, MoETile *tiles,
+                                   int32_t *n_tiles, int32_t tile_rows, int8_t *xq, float *xs,
+                                   hipStream_t s) {
+  const int64_t pairs = t * topk;
+  if (pairs > kRouteOneGroupPairs || k > 64 * 8 * 8) {
+    const hipError_t e = launch_act_int8(x, t, k, xq, xs, s);
+    if (e != hipSuccess) return e;
+    return launch_route(ids, pairs, topk, n_experts, counts, offsets, perm, inv, tiles, n_tiles,
+                        tile_rows, nullptr, s);
+  }
+  if (n_experts < 1 || n_experts > kMaxExperts || pairs < 0) return hipErrorInvalidValue;
+  const int64_t groups = 1 + (t + kRouteWaves - 1) / kRouteWaves;
+  hipLaunchKernelGGL(i8_route_act_kernel, dim3(static_cast<unsigned>(groups)),
+                     dim3(kRouteThreads), 0, s, ids, pairs, n_experts, counts, offsets, perm, inv,
+                     tiles, n_tiles, tile_rows, x, t, static_cast<int32_t>(k),
+                     static_cast<int32_t>(int8_padded_k(k)), xq, xs);
   return hipGetLastError();
 }
 

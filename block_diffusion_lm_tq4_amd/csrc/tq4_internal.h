@@ -350,6 +350,13 @@ hipError_t launch_moe_int8_direct(const uint16_t *x, int64_t t, int64_t k, const
                                   const float *gates, int32_t topk, int32_t n_experts,
                                   const int8_t *w1, const float *s1, int64_t n1, const int8_t *w2,
                                   const float *s2, uint16_t *h, float *out, hipStream_t s);
+// The MoE layer's first step: launch_route's outputs for the pairs, and x's
+// codes and scales.
+hipError_t launch_moe_int8_prepare(const uint16_t *x, int64_t t, int64_t k, const int32_t *ids,
+                                   int32_t topk, int32_t n_experts, int32_t *counts,
+                                   int32_t *offsets, int32_t *perm, int32_t *inv, MoETile *tiles,
+                                   int32_t *n_tiles, int32_t tile_rows, int8_t *xq, float *xs,
+                                   hipStream_t s);
 // Grouped products over stacked int8 experts (expert e's rows at e * n of the
 // [E * n, k] cache).  mode 0 (up): rows gathered as perm[row] / topk; out is
 // bf16 [pairs][n], relu(u)^2.  a_rows: rows of aq.  mode 1 (down): bucket rows; out is fp32
