@@ -359,7 +359,8 @@ size_t tq4_linear_int8_workspace_size(int64_t m, int64_t k, int64_t n);
 /* y[m, n] = (sum_k xq[m, k] wq[n, k]) * sx[m] * sw[n]: x quantized per call
  * (tq4_act_int8, into the workspace), the weights from a cache built by
  * tq4_int8_cache or tq4_int8_cache_bf16.  The sum is exact, the two products
- * with the scales are fp32 in this order; deterministic.  Rows of x that hold
+ * with the scales are fp32 in this order; deterministic.  (A sum times sx
+ * past fp32's range is infinite, whatever sw.)  Rows of x that hold
  * a NaN or an infinity, and such rows of the weights, give NaN.
  *   x_bf16 : [m, k] bf16 bit patterns, device, 16-byte aligned
  *   cache  : for this [n, k], device, 16-byte aligned
@@ -419,8 +420,9 @@ size_t tq4_moe_grouped_int8_workspace_size(int64_t t, int32_t topk, int32_t n_ex
  *   workspace: tq4_moe_grouped_int8_workspace_size(...) bytes, device,
  *              256-byte aligned, no initial contents required
  * Steps: activation quantization, bucketing, grouped up projection with
- * relu^2, quantization of the hidden rows, grouped down projection, and the
- * per-token weighted sum in slot order (fp32).  Deterministic.  Errors: as
+ * relu^2, quantization of the hidden rows, grouped down projection (sum * scale
+ * of the hidden row * scale of W2's, fp32 in this order), and the per-token
+ * weighted sum in slot order (fp32).  Deterministic.  Errors: as
  * tq4_moe_grouped, plus TQ4_E_SHAPE when t * kp or t * topk * n1p reach 2^31
  * (kp, n1p: k, n1 padded to 64) or k or n1 exceed 131072. */
 int tq4_moe_grouped_int8(const uint16_t *x_bf16, int64_t t, int64_t k, const int32_t *topk_ids,
