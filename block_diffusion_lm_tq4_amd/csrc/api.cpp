@@ -655,6 +655,19 @@ bool int8_sizes_ok(int64_t rows, int64_t k) {
   return rows >= 0 && rows <= INT32_MAX && k >= 0 && k % 32 == 0 && k <= kI8MaxK;
 }
 
+// Rows of a product's operands: a grid's threads count in 32 bits.
+constexpr int64_t kI8MaxLinearRows = 1 << 24;
+
+bool int8_linear_sizes_ok(int64_t m, int64_t k, int64_t n) {
+  return int8_sizes_ok(m, k) && int8_sizes_ok(n, k) && m <= kI8MaxLinearRows &&
+         n <= kI8MaxLinearRows;
+}
+
+bool overlap(const void *a, uint64_t a_bytes, const void *b, uint64_t b_bytes) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + b_bytes && b0 < a0 + a_bytes;
+}
+
 size_t int8_codes_bytes(int64_t rows, int64_t k) {
   return static_cast<size_t>(rows) * static_cast<size_t>(tq4::int8_padded_k(k));
 }
@@ -667,7 +680,7 @@ int linear_int8_impl(const uint16_t *x_bf16, const int8_t *x_codes, const float 
                      int64_t m, int64_t k, const uint8_t *cache, int64_t n,
                      const tq4::Tail &tail, void *y, void *workspace, size_t workspace_bytes,
                      void *stream) {
-  if (!int8_sizes_ok(m, k) || !int8_sizes_ok(n, k)) return TQ4_E_SHAPE;
+  if (!int8_linear_sizes_ok(m, k, n)) return TQ4_E_SHAPE;
   if (m == 0 || n == 0) return TQ4_OK;
   const int st = linear_tail_args(m, n, tail, y);
   if (st != TQ4_OK) return st;
@@ -679,15 +692,21 @@ int linear_int8_impl(const uint16_t *x_bf16, const int8_t *x_codes, const float 
                                : tq4::launch_tail_only(tail, m, n, yf, s));
   if (cache == nullptr) return TQ4_E_NULL;
   if (!aligned(cache, 16)) return TQ4_E_ALIGN;
+  const uint64_t y_bytes = static_cast<uint64_t>(m) * n * (tail.bf16 ? 2 : 4);
   if (x_bf16 != nullptr) {
     if (!aligned(x_bf16, 16)) return TQ4_E_ALIGN;
-    if (tq4::int8_direct_fits(m, k))
+    const bool direct = tq4::int8_direct_fits(m, k);
+    if (!direct) {
+      const int ws = check_workspace(workspace, workspace_bytes,
+                                     tq4_linear_int8_workspace_size(m, k, n));
+      if (ws != TQ4_OK) return ws;
+    }
+    // a single row is read by workgroups while others store
+    if (overlap(x_bf16, static_cast<uint64_t>(m) * k * 2, y, y_bytes)) return TQ4_E_SHAPE;
+    if (direct)
       return device_status(tq4::launch_linear_int8_direct(
           x_bf16, m, k, reinterpret_cast<const int8_t *>(cache), int8_scales(cache, n, k), n, tail,
           y, s));
-    const int ws = check_workspace(workspace, workspace_bytes,
-                                   tq4_linear_int8_workspace_size(m, k, n));
-    if (ws != TQ4_OK) return ws;
     int8_t *xq = static_cast<int8_t *>(workspace);
     float *xs = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                           align_up(int8_codes_bytes(m, k)));
@@ -698,6 +717,9 @@ int linear_int8_impl(const uint16_t *x_bf16, const int8_t *x_codes, const float 
   } else {
     if (x_codes == nullptr || x_scales == nullptr) return TQ4_E_NULL;
     if (!aligned(x_codes, 16) || !aligned(x_scales, 4)) return TQ4_E_ALIGN;
+    if (overlap(x_codes, int8_codes_bytes(m, k), y, y_bytes) ||
+        overlap(x_scales, static_cast<uint64_t>(m) * sizeof(float), y, y_bytes))
+      return TQ4_E_SHAPE;
   }
   return device_status(tq4::launch_linear_int8(x_codes, x_scales, m, k,
                                                reinterpret_cast<const int8_t *>(cache),
@@ -708,7 +730,7 @@ int linear_int8_impl(const uint16_t *x_bf16, const int8_t *x_codes, const float 
 int linear_int8_bf16(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache,
                      int64_t n, const tq4::Tail &tail, void *y, void *workspace,
                      size_t workspace_bytes, void *stream) {
-  if (x_bf16 == nullptr && m > 0 && n > 0 && k > 0 && int8_sizes_ok(m, k) && int8_sizes_ok(n, k))
+  if (x_bf16 == nullptr && m > 0 && n > 0 && k > 0 && int8_linear_sizes_ok(m, k, n))
     return TQ4_E_NULL;
   return linear_int8_impl(x_bf16, nullptr, nullptr, m, k, cache, n, tail, y, workspace,
                           workspace_bytes, stream);
@@ -753,7 +775,7 @@ int tq4_act_int8(const uint16_t *x_bf16, int64_t m, int64_t k, int8_t *codes, fl
 }
 
 size_t tq4_linear_int8_workspace_size(int64_t m, int64_t k, int64_t n) {
-  if (!int8_sizes_ok(m, k) || !int8_sizes_ok(n, k)) return 0;
+  if (!int8_linear_sizes_ok(m, k, n)) return 0;
   if (m == 0 || n == 0 || k == 0 || tq4::int8_direct_fits(m, k)) return 0;
   return align_up(int8_codes_bytes(m, k)) + align_up(static_cast<size_t>(m) * sizeof(float));
 }

@@ -641,7 +641,7 @@ def _linear_int8(fn, x, cache, n, tail, out, workspace, ydtype):
 def linear_int8(x: torch.Tensor, cache: torch.Tensor, n: int, out: torch.Tensor | None = None,
                 workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y = x . W^T in int8 from the cache of an [n, k] matrix, fp32 [m, n]
-    (tq4_linear_int8)."""
+    (tq4_linear_int8).  `out` may not overlap x."""
     return _linear_int8("tq4_linear_int8", x, cache, n, None, out, workspace, torch.float32)
 
 
@@ -650,7 +650,7 @@ def linear_int8_epilogue(x: torch.Tensor, cache: torch.Tensor, n: int,
                          out: torch.Tensor | None = None,
                          workspace: torch.Tensor | None = None) -> torch.Tensor:
     """linear_int8 + bias + residual, fp32 [m, n] (tq4_linear_int8_epilogue);
-    the residual may be `out` itself."""
+    the residual may be `out` itself, which may not overlap x."""
     return _linear_int8("tq4_linear_int8_epilogue", x, cache, n, (bias, residual), out, workspace,
                         torch.float32)
 
@@ -661,7 +661,8 @@ def linear_int8_epilogue_bf16(x: torch.Tensor, cache: torch.Tensor, n: int,
                               out: torch.Tensor | None = None,
                               workspace: torch.Tensor | None = None) -> torch.Tensor:
     """bf16(linear_int8 + bias + residual), bf16 [m, n], the residual bf16
-    (tq4_linear_int8_epilogue_bf16); it may be `out` itself."""
+    (tq4_linear_int8_epilogue_bf16); it may be x, or `out`, which may not overlap
+    x."""
     return _linear_int8("tq4_linear_int8_epilogue_bf16", x, cache, n, (bias, residual), out,
                         workspace, torch.bfloat16)
 

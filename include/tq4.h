@@ -366,8 +366,11 @@ size_t tq4_linear_int8_workspace_size(int64_t m, int64_t k, int64_t n);
  *   cache  : for this [n, k], device, 16-byte aligned
  *   y      : [m, n] fp32, device, 4-byte aligned, overwritten
  *   workspace : tq4_linear_int8_workspace_size(m, k, n) bytes, 256-byte
- *               aligned
- * Errors: as tq4_linear.  m == 0 or n == 0 is a no-op; k == 0 writes zeros. */
+ *               aligned (may be NULL when that size is 0, as for m == 1 with
+ *               k <= 8192)
+ * Errors: as tq4_linear, plus TQ4_E_SHAPE for m or n above 2^24 and for a y
+ * that overlaps x (a residual may be x; the output may not).  m == 0 or n == 0
+ * is a no-op; k == 0 writes zeros. */
 int tq4_linear_int8(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache,
                     int64_t n, float *y, void *workspace, size_t workspace_bytes, void *stream);
 

@@ -165,3 +165,30 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="device"):
         ops.moe_grouped_int8(x, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), cache,
                              cache, 1, 32)
+
+
+def test_linear_output_may_not_be_its_input(L):
+    """A residual that is x and an output that is x too: some rows would be read
+    after others were stored."""
+    far = FAKE + (1 << 30)
+    for m, k, n in ((1, 64, 64), (40, 64, 64)):
+        ws = L.tq4_linear_int8_workspace_size(m, k, n)
+        for y in (FAKE, FAKE + 4, FAKE + 2 * m * k - 4, FAKE - 4):
+            assert L.tq4_linear_int8(FAKE, m, k, far, n, y, 2 * far, ws, None) == E_SHAPE
+            assert L.tq4_linear_int8_epilogue(FAKE, m, k, far, n, None, None, y, 2 * far, ws,
+                                              None) == E_SHAPE
+            assert L.tq4_linear_int8_epilogue_bf16(FAKE, m, k, far, n, None, y, y, 2 * far, ws,
+                                                   None) == E_SHAPE
+        for y in (FAKE, FAKE + m * k - 4, FAKE - 4):
+            assert L.tq4_linear_int8_quantized(FAKE, 3 * far, m, k, far, n, y, None) == E_SHAPE
+        assert L.tq4_linear_int8_quantized(3 * far, FAKE, m, k, far, n, FAKE, None) == E_SHAPE
+
+
+def test_linear_row_limit(L):
+    big = (1 << 24) + 1
+    for m, n in ((big, 8), (8, big)):
+        assert L.tq4_linear_int8_workspace_size(m, 64, n) == 0
+        assert L.tq4_linear_int8(FAKE, m, 64, FAKE, n, FAKE, FAKE, 1 << 40, None) == E_SHAPE
+        assert L.tq4_linear_int8_quantized(FAKE, FAKE, m, 64, FAKE, n, FAKE, None) == E_SHAPE
+    assert L.tq4_linear_int8_workspace_size(1 << 24, 64, 8) > 0
+    assert L.tq4_int8_cache_size(big, 64) == big * 68              # a cache may have more
