@@ -7,6 +7,8 @@ in the library's kernels; torch only provides memory and streams.
 
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from ._lib import check, lib
@@ -607,6 +609,7 @@ def act_int8(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     return codes, scales
 
 
+@functools.lru_cache(maxsize=4096)  # the call takes 0.6 us, the lookup 0.1
 def linear_int8_workspace_size(m: int, k: int, n: int) -> int:
     return int(lib().tq4_linear_int8_workspace_size(m, k, n))
 
@@ -633,7 +636,7 @@ def _linear_int8(fn, x, cache, n, tail, out, workspace, ydtype):
     else:
         _arg_on(out, "out", ydtype, dev)
         _require(tuple(out.shape) == (m, n), "out must be [m, n]")
-    held, ws, ws_size = _scratch(workspace, lib().tq4_linear_int8_workspace_size(m, k, n), dev)
+    held, ws, ws_size = _scratch(workspace, linear_int8_workspace_size(m, k, n), dev)
     _call(fn, dev, x.data_ptr(), m, k, cache.data_ptr(), n, *ptrs, out.data_ptr(), ws, ws_size)
     return out
 
@@ -690,6 +693,7 @@ def linear_int8_quantized(x_codes: torch.Tensor, x_scales: torch.Tensor, k: int,
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_grouped_int8_workspace_size(t: int, topk: int, n_experts: int, n1: int, k: int) -> int:
     return int(lib().tq4_moe_grouped_int8_workspace_size(t, topk, n_experts, n1, k))
 
