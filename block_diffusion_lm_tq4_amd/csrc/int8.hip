@@ -26,6 +26,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "tq4_internal.h"
 
 namespace tq4 {
@@ -827,8 +829,8 @@ __global__ __launch_bounds__(128 * kDirectSlots) void i8_direct_down_kernel(I8Ar
 // of 16 * NS outputs.  Stores are non-temporal: nothing reads the output before
 // the operands that it would push out of the caches are needed (4096 x 2688 x
 // 8192: 107 -> 96 us, the up product of 1024 tokens on 128 experts 134.5 -> 124).
-// Residual values of the next 16 rows are loaded before the stores of these,
-// since a wait for a load is also one for every store before it.
+// Residual values of later rows are loaded before the stores of these, since a
+// wait for a load is also one for every store before it.
 template <int NS>
 constexpr int tile_store_bytes() {
   return 2 * 16 * (16 * NS + 4) * 4;
@@ -850,39 +852,59 @@ __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], u
   const int grp = lane / 16;
   const bool has_bias = MODE == kI8Dense && g.tail.bias != nullptr;
   const bool has_res = MODE == kI8Dense && g.tail.residual != nullptr;
-  // this lane's columns in the row image are the same for every group of rows
-  // when a row is a divisor of 64 * E outputs, which it is for NS = 1, 2, 4
-  // (and 8 with E = 4 loops twice over half-waves' rows)
-  float res[kGroups][E];
+  // Residual values as they lie in memory, loaded several groups of 16 rows
+  // ahead of their use, since each is a trip to HBM: as many as 40 registers
+  // hold (the operands' are free by now; with more the largest tile spills).
+  // One group ahead, the bf16 residual of 1024 x 2688 x 4096 made the product 24.0
+  // us, so 18.9; that of 4096 x 8192 x 2688 89.5 and 82.
+  using Raw = std::conditional_t<VEC, std::conditional_t<BF16, uintx2, floatx4>, float>;
+  constexpr int kWords = kGroups * static_cast<int>(sizeof(Raw)) / 4;
+  constexpr int kAhead = 40 / kWords < MS ? 40 / kWords : MS;
+  static_assert(kAhead >= 1, "a group of rows fits");
+  Raw res[MODE == kI8Dense ? kAhead : 1][kGroups];
   auto load_res = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
       const int f = 64 * E * q + E * lane;
       const int row = 16 * WM * i + f / kCols;
       const int64_t n = n0 + f % kCols;
-#pragma unroll
-      for (int v = 0; v < E; ++v) res[q][v] = 0.f;
+      Raw &d = res[i % kAhead][q];
+      d = Raw{};
       if (row < rows && n < g.n) {
         const int64_t at = (m0 + row) * g.n + n;
-        if constexpr (VEC && BF16) {
-          const uintx2 d =
-              *reinterpret_cast<const uintx2 *>(static_cast<const uint16_t *>(g.tail.residual) + at);
-          res[q][0] = __uint_as_float(d.x << 16);
-          res[q][1] = __uint_as_float(d.x & 0xFFFF0000u);
-          res[q][2] = __uint_as_float(d.y << 16);
-          res[q][3] = __uint_as_float(d.y & 0xFFFF0000u);
-        } else if constexpr (VEC) {
-          const floatx4 d =
-              *reinterpret_cast<const floatx4 *>(static_cast<const float *>(g.tail.residual) + at);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) res[q][v] = d[v];
-        } else {
-          res[q][0] = tail_residual_as<BF16>(g.tail.residual, at);
-        }
+        if constexpr (VEC && BF16)
+          d = *reinterpret_cast<const Raw *>(static_cast<const uint16_t *>(g.tail.residual) + at);
+        else if constexpr (VEC)
+          d = *reinterpret_cast<const Raw *>(static_cast<const float *>(g.tail.residual) + at);
+        else
+          d = tail_residual_as<BF16>(g.tail.residual, at);
       }
     }
   };
-  if (has_res) load_res(0);
+  auto res_at = [&](int i, int q, int v) __attribute__((always_inline)) {
+    const Raw &d = res[i % kAhead][q];
+    if constexpr (VEC && BF16) {
+      const uint32_t w = d[v / 2];
+      return __uint_as_float(v % 2 == 0 ? w << 16 : w & 0xFFFF0000u);
+    } else if constexpr (VEC) {
+      return static_cast<float>(d[v]);
+    } else {
+      return d;
+    }
+  };
+  float bias[kGroups][E];
+  if constexpr (MODE == kI8Dense) {
+    if (has_res) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) load_res(i);
+    }
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      const int64_t n = n0 + (64 * E * q + E * lane) % kCols;
+#pragma unroll
+      for (int v = 0; v < E; ++v) bias[q][v] = has_bias && n < g.n ? g.tail.bias[n + v] : 0.f;
+    }
+  }
   if constexpr (MODE == kI8Up) {
     // the row image is bf16: 2 * kStride bytes per row, eight outputs per lane
     bool tame = true;
@@ -942,15 +964,16 @@ __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], u
         val[q][0] = *src;
       }
       if constexpr (MODE == kI8Dense) {
-        const int64_t n = n0 + f % kCols;
 #pragma unroll
         for (int v = 0; v < E; ++v) {
-          if (has_bias) val[q][v] += n < g.n ? g.tail.bias[n + v] : 0.f;
-          if (has_res) val[q][v] += res[q][v];
+          if (has_bias) val[q][v] += bias[q][v];
+          if (has_res) val[q][v] += res_at(i, q, v);
         }
       }
     }
-    if (has_res && i + 1 < MS) load_res(i + 1);
+    if constexpr (MODE == kI8Dense) {
+      if (has_res && i + kAhead < MS) load_res(i + kAhead);
+    }
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
       const int f = 64 * E * q + E * lane;
@@ -1264,6 +1287,10 @@ hipError_t launch_skinny_cfg(I8Args g, int64_t max_tiles, hipStream_t s) {
 // sweeps over m = 32 .. 4096 at (k, n) = (2688, 8192), (8192, 2688) and (1856,
 // 2688); the order it gives was that of the measured times at all of them, to
 // within 8 %.)
+// Where each compute unit gets one of the two largest tiles they are within 5 %
+// of each other, either way (192 rows / 256: 4099 x 2688 x 2690 38.9 / 40.8 us,
+// 1025 x 2688 x 8192 30.4 / 32.2, 6100 x 1856 x 2000 30.8 / 29.6, 4096 x 8192 x
+// 2688 83.4 / 81.3, with a bf16 residual 83.1 / 82.9).
 int pick_tile(int64_t m, int64_t n) {
   struct Cost {
     int tm, tn, slots;
