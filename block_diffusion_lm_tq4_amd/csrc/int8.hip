@@ -634,9 +634,9 @@ __global__ __launch_bounds__(64 * KW) void i8_skinny_kernel(I8Args g) {
 // is that of the register stream above, the row's codes broadcast to all
 // sixteen rows of the operand.
 //
-// m = 1, 2688 x 8192: 8.3 us against 9.0 for quantizer and product one after
-// the other, and one launch for the host instead of two (8.3 against 12.2 us
-// a call).  From two rows on the wave's own quantization costs more than it
+// m = 1, 2688 x 8192: 7.4 us against 8.6 for quantizer and product one after
+// the other, and one launch for the host instead of two (8.0 against 12.7 us
+// a call); 8192 x 2688 7.7 against 10.8.  From two rows on the wave's own quantization costs more than it
 // saves (10.2 against 9.1 us).
 
 constexpr int kDirectVecs = 16;   // pieces of 8 values per lane: k <= 8192
@@ -1431,8 +1431,8 @@ hipError_t launch_linear_int8_direct(const uint16_t *x, int64_t m, int64_t k, co
 }
 
 // Up to 12 pairs (two tokens of six slots), and the row and step limits of the
-// kernels.  128 experts of 1856 x 2688, top-6: one token 25 us against 33 for
-// the batched steps, two 39 against 44, four 65 against 62 (the batched steps
+// kernels.  128 experts of 1856 x 2688, top-6: one token 24 us against 31 for
+// the batched steps, two 37 against 42, four 65 against 62 (the batched steps
 // read an expert that two tokens share once).
 bool int8_moe_direct_fits(int64_t t, int32_t topk, int64_t n1, int64_t k) {
   return t * topk <= 12 && topk <= kDirectSlots && k <= 64 * 8 * kDirectVecs &&
@@ -1517,14 +1517,14 @@ hipError_t launch_linear_int8(const int8_t *xq, const float *xs, int64_t m, int6
 
 // Rows per tile by the average number of rows per expert, from sweeps of the
 // two products over 128 experts of 1856 x 2688 (up + down, us; uniform
-// routing, then Zipf): 6 rows 16-row tiles 278 / 260, 64-row tiles 235 / 203;
-// 24 rows 64-row 257 / 277, 128-row 265 / 275; 48 rows 280 / 326 and 287 /
-// 309; 96 rows 128-row 325 / 380, 256-row 354 / 402; 140 rows 460 / 459 and
-// 382 / 469.  At 3 rows 16-row tiles take 226.
+// routing / Zipf): 1.5 rows 16-row tiles 176 / 119, 64-row tiles 183 / 125; 2.25
+// rows 207 / 161 and 206 / 153; 3 rows 226 / 171 and 219 / 155; 24 rows 64-row
+// 252 / 275, 128-row 256 / 265; 33 rows 260 / 296 and 261 / 279; 96 rows
+// 128-row 296 / 375, 256-row 330 / 386; 136 rows 436 / 435 and 357 / 442.
 int int8_moe_tile_rows(int64_t pairs, int32_t n_experts) {
   const int64_t e = n_experts;
-  if (pairs <= 4 * e) return 16;
-  if (pairs <= 32 * e) return 64;
+  if (pairs <= 2 * e) return 16;
+  if (pairs <= 20 * e) return 64;
   return pairs <= 128 * e ? 128 : 256;
 }
 

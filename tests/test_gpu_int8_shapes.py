@@ -110,7 +110,8 @@ MOE = [(2, 8, 6, 96, 64), (13, 5, 1, 96, 64), (12, 5, 1, 96, 64), (1, 12, 8, 64,
        (1, 12, 9, 64, 96), (1, 3, 2, 2048, 64), (1, 3, 2, 2080, 64), (1, 3, 2, 64, 4096),
        (1, 3, 2, 64, 4128), (3, 4, 4, 1856, 2688), (30, 16, 2, 544, 608), (60, 4, 2, 544, 608),
        (260, 4, 2, 544, 608), (300, 2, 1, 288, 544), (700, 2, 1, 544, 608), (700, 2, 1, 608, 544),
-       (20, 3, 2, 64, 4128), (4100, 5, 2, 64, 96), (4095, 3, 2, 32, 64), (4096, 3, 2, 64, 32)]
+       (20, 3, 2, 64, 4128), (4100, 5, 2, 64, 96), (4095, 3, 2, 32, 64), (4096, 3, 2, 64, 32),
+       (14, 8, 1, 96, 64), (12, 16, 2, 352, 416), (20, 16, 1, 64, 4128), (13, 40, 3, 2080, 608)]
 
 
 @pytest.mark.parametrize("t,e,topk,n1,k", MOE)
