@@ -768,7 +768,12 @@ int tq4_int8_cache_bf16(const uint16_t *w_bf16, int64_t n, int64_t k, uint8_t *c
 int tq4_act_int8(const uint16_t *x_bf16, int64_t m, int64_t k, int8_t *codes, float *scales,
                  void *stream) {
   if (!int8_sizes_ok(m, k)) return TQ4_E_SHAPE;
-  if (m == 0 || k == 0) return TQ4_OK;
+  if (m == 0) return TQ4_OK;
+  if (k == 0) {  // empty rows are zero rows
+    if (scales == nullptr) return TQ4_OK;
+    if (!aligned(scales, 4)) return TQ4_E_ALIGN;
+    return device_status(tq4::launch_fill_zero(scales, m, as_stream(stream)));
+  }
   if (x_bf16 == nullptr || codes == nullptr || scales == nullptr) return TQ4_E_NULL;
   if (!aligned(x_bf16, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return TQ4_E_ALIGN;
   return device_status(tq4::launch_act_int8(x_bf16, m, k, codes, scales, as_stream(stream)));

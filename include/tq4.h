@@ -348,7 +348,7 @@ int tq4_int8_cache_bf16(const uint16_t *w_bf16, int64_t n, int64_t k, uint8_t *c
 
 /* Quantize bf16 activations [m, k] (device, 16-byte aligned) as above: codes
  * [m][kp] (device, 16-byte aligned) and scales [m] fp32 (device).  Errors as
- * tq4_int8_cache. */
+ * tq4_int8_cache; k == 0 writes zero scales, if scales is not NULL. */
 int tq4_act_int8(const uint16_t *x_bf16, int64_t m, int64_t k, int8_t *codes, float *scales,
                  void *stream);
 

@@ -192,3 +192,9 @@ def test_linear_row_limit(L):
         assert L.tq4_linear_int8_quantized(FAKE, FAKE, m, 64, FAKE, n, FAKE, None) == E_SHAPE
     assert L.tq4_linear_int8_workspace_size(1 << 24, 64, 8) > 0
     assert L.tq4_int8_cache_size(big, 64) == big * 68              # a cache may have more
+
+
+def test_act_of_empty_rows(L):
+    assert L.tq4_act_int8(None, 0, 0, None, None, None) == OK
+    assert L.tq4_act_int8(None, 4, 0, None, None, None) == OK
+    assert L.tq4_act_int8(None, 4, 0, None, MIS, None) == E_ALIGN

@@ -101,6 +101,20 @@ def test_linear_past_32_bits(dev):
     del q, s, y
 
 
+def test_nothing_to_do(dev):
+    """No rows, and rows without elements."""
+    codes, scales = _ops().act_int8(torch.zeros(0, 64, dtype=torch.bfloat16, device=dev))
+    assert codes.shape == (0, 64) and scales.shape == (0,)
+    for m in (1, 300):
+        codes, scales = _ops().act_int8(torch.zeros(m, 0, dtype=torch.bfloat16, device=dev))
+        assert codes.shape == (m, 0) and (scales == 0).all()
+    c1, c2, _, _ = _experts(dev, 2, 64, 32, seed=0)
+    none = torch.zeros(0, 1, device=dev)
+    out = _ops().moe_grouped_int8(torch.zeros(0, 32, dtype=torch.bfloat16, device=dev),
+                                  none.to(torch.int32), none, c1, c2, 2, 64)
+    assert out.shape == (0, 32)
+
+
 # ---- MoE ---------------------------------------------------------------------
 
 # (tokens, experts, topk, n1, k): the single-token form's limits on pairs, topk, n1
