@@ -1330,7 +1330,12 @@ hipError_t launch_act_int8(const uint16_t *x, int64_t m, int64_t k, int8_t *code
   if (m == 0 || k == 0) return hipSuccess;
   const int32_t k32 = static_cast<int32_t>(k);
   const int32_t kp = static_cast<int32_t>(int8_padded_k(k));
-  if (m >= 1024 && k <= 64 * 8 * 8) {
+  // A wave per row needs no barrier, a workgroup per row has the shorter chain
+  // (us, wave / workgroup: k = 1856: 1024 rows 4.3 / 3.4, 2048 5.0 / 5.1, 4096 7.1 /
+  // 7.8, 24576 24 / 36; k = 2688: 4096 rows 10.0 / 8.9, 24576 37 / 42; k = 8192: 4096
+  // rows 23 / 18).  Four pieces of a row per lane where they hold it, else eight
+  // (24 / 28 and 40 / 37).
+  if ((m >= 4096 && k <= 64 * 8 * 4) || (m >= 12288 && k <= 64 * 8 * 8)) {
     const int64_t groups = (m + 3) / 4;
     const dim3 grid(static_cast<unsigned>(groups < 65536 ? groups : 65536));
     if (k <= 64 * 8 * 4)

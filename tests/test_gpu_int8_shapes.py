@@ -101,6 +101,19 @@ def test_linear_past_32_bits(dev):
     del q, s, y
 
 
+@pytest.mark.parametrize("m,k", [(4100, 96), (4097, 1856), (5000, 2080), (12300, 2112),
+                                 (70000, 32), (1025, 4096), (1024, 4128)])
+def test_act_codes_of_many_rows(dev, m, k):
+    x = _acts(m, k, seed=m + k)
+    x[m // 2] = 0
+    x[m - 1, k - 1] = 0x7FC0
+    codes, scales = _ops().act_int8(_bf16(x, dev))
+    ref, ref_s = O.act_int8(x)
+    codes = codes.cpu().numpy()
+    assert np.array_equal(codes[:, :k], ref) and not codes[:, k:].any()
+    assert np.array_equal(scales.cpu().numpy(), ref_s.astype(np.float32), equal_nan=True)
+
+
 def test_nothing_to_do(dev):
     """No rows, and rows without elements."""
     codes, scales = _ops().act_int8(torch.zeros(0, 64, dtype=torch.bfloat16, device=dev))
