@@ -126,6 +126,14 @@ __device__ inline void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// A chosen expert's weight from its score p and the sum of the token's.  The
+// quotient comes first: a sum below 2^-1022, as of experts that only their bias
+// brought in, has no finite reciprocal.
+__device__ inline float weight(double p, double total, const RouterConfig &cfg) {
+  if (cfg.renormalize) p = total > 0.0 ? p / total : 0.0;
+  return static_cast<float>(p * static_cast<double>(cfg.scale));
+}
+
 // Writes the token's ids[0 .. topk) and w[0 .. topk); gv: kMaxExperts doubles of
 // the wave's own LDS.  n_experts <= 64 PER, topk <= 64 SLOTS.
 template <int PER, int SLOTS>
@@ -248,14 +256,12 @@ __device__ inline void route_token_f64(const float *__restrict__ row, const Rout
         slot_id[q] = bi;
       }
   }
-  double f = static_cast<double>(cfg.scale);
-  if (cfg.renormalize) f = total > 0.0 ? f / total : 0.0;
 #pragma unroll
   for (int q = 0; q < SLOTS; ++q) {
     const int j = lane + 64 * q;
     if (j < cfg.topk) {
       ids[j] = slot_id[q];
-      w[j] = static_cast<float>(slot_w[q] * f);
+      w[j] = weight(slot_w[q], total, cfg);
     }
   }
 }
@@ -602,14 +608,10 @@ __global__ __launch_bounds__(64 * kFastWaves) void router_fast_kernel(
   }
   const bool chosen = slot < cfg.topk;
   if (!found) p = 0.0;
-  double f = static_cast<double>(cfg.scale);
-  if (cfg.renormalize) {
-    const double total = row_sum_f64(chosen ? p : 0.0);
-    f = total > 0.0 ? f / total : 0.0;
-  }
+  const double total = cfg.renormalize ? row_sum_f64(chosen ? p : 0.0) : 0.0;
   if (real && chosen) {
     ids[tok * cfg.topk + slot] = my_id;
-    w[tok * cfg.topk + slot] = static_cast<float>(p * f);
+    w[tok * cfg.topk + slot] = weight(p, total, cfg);
   }
 
   // unclear tokens again, one after another, by the whole wave

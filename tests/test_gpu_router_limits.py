@@ -1,0 +1,40 @@
+"""The scored router at the ends of its range: scores below fp64's normal range,
+slots without an expert, biases that bar an expert, and more tokens than one
+launch holds.  Ids are equal to the fp64 oracle's and weights one rounding
+(2^-24 relative, and fp32's last bit where they are subnormal) of its own.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from test_gpu_int8 import _check_router, _ops, dev  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# four tokens a wave; that and its fp64 pass (equal biases: the border is not
+# clear); a wave a token, by its slots and by its groups
+FORMS = [(64, 4, 1, 1, False), (64, 4, 1, 1, True), (256, 8, 8, 4, False), (64, 15, 1, 1, False),
+         (102, 6, 17, 4, False)]
+
+
+@pytest.mark.parametrize("e,topk,groups,keep,equal", FORMS)
+@pytest.mark.parametrize("scale", [1.0, 2.5])
+def test_router_renormalizes_scores_below_the_normal_range(dev, e, topk, groups, keep, equal,
+                                                           scale):
+    """A bias brings in experts whose softmax scores are fp64 subnormals: the sum's
+    reciprocal is infinite, its quotients are not.  Scores are above e^-716 > 2^-1034
+    and so have 40 bits, of which two exponentials may differ in the last."""
+    rng = np.random.default_rng(e + topk)
+    lg = (-714.0 - 1.9 * rng.random((40, e))).astype(np.float32)
+    lg[:, ::3] = -np.abs(rng.standard_normal((40, lg[:, ::3].shape[1])))
+    lg[:, 0] = 0
+    bias = np.full(e, 3.0, np.float32) if equal else rng.permutation(e).astype(np.float32) + 3
+    bias[::3] = -3
+    ids, w = _check_router(dev, lg, topk, score="softmax", bias=bias, n_groups=groups,
+                           topk_groups=keep, renormalize=True, scale=scale)
+    assert (ids.cpu().numpy() % 3 != 0).all()
+    total = w.cpu().numpy().astype(np.float64).sum(axis=1)
+    assert (np.abs(total - scale) <= scale * topk * 2.0 ** -24).all()
