@@ -126,11 +126,16 @@ __device__ inline void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// A chosen expert's weight from its score p and the sum of the token's.  The
-// quotient comes first: a sum below 2^-1022, as of experts that only their bias
-// brought in, has no finite reciprocal.
-__device__ inline float weight(double p, double total, const RouterConfig &cfg) {
-  if (cfg.renormalize) p = total > 0.0 ? p / total : 0.0;
+// A slot's weight from its expert's score p and the sum of the token's; 0 without
+// an expert, and where the sum is, whatever the factor.  The quotient comes
+// first: a sum below 2^-1022, as of experts that only their bias brought in, has
+// no finite reciprocal.
+__device__ inline float weight(bool found, double p, double total, const RouterConfig &cfg) {
+  if (!found) return 0.f;
+  if (cfg.renormalize) {
+    if (!(total > 0.0)) return 0.f;
+    p /= total;
+  }
   return static_cast<float>(p * static_cast<double>(cfg.scale));
 }
 
@@ -261,7 +266,7 @@ __device__ inline void route_token_f64(const float *__restrict__ row, const Rout
     const int j = lane + 64 * q;
     if (j < cfg.topk) {
       ids[j] = slot_id[q];
-      w[j] = weight(slot_w[q], total, cfg);
+      w[j] = weight(slot_id[q] >= 0, slot_w[q], total, cfg);
     }
   }
 }
@@ -611,7 +616,7 @@ __global__ __launch_bounds__(64 * kFastWaves) void router_fast_kernel(
   const double total = cfg.renormalize ? row_sum_f64(chosen ? p : 0.0) : 0.0;
   if (real && chosen) {
     ids[tok * cfg.topk + slot] = my_id;
-    w[tok * cfg.topk + slot] = weight(p, total, cfg);
+    w[tok * cfg.topk + slot] = weight(found, p, total, cfg);
   }
 
   // unclear tokens again, one after another, by the whole wave

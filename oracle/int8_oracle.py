@@ -123,7 +123,9 @@ def router_scored(logits, topk, score="softmax", bias=None, n_groups=1, topk_gro
         for j, (_, x) in enumerate(order):
             ids[i, j] = x
             w[i, j] = p[x]
+        if not order or renormalize and not w[i].sum() > 0:
+            continue  # zeros, whatever the factor
         if renormalize:
-            s = w[i].sum()
-            w[i] = w[i] / s if s > 0 else 0.0
-    return ids, w * scale
+            w[i] /= w[i].sum()
+        w[i, :len(order)] *= scale
+    return ids, w

@@ -38,3 +38,26 @@ def test_router_renormalizes_scores_below_the_normal_range(dev, e, topk, groups,
     assert (ids.cpu().numpy() % 3 != 0).all()
     total = w.cpu().numpy().astype(np.float64).sum(axis=1)
     assert (np.abs(total - scale) <= scale * topk * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,topk,groups,keep", [(6, 5, 1, 1), (64, 15, 1, 1), (34, 4, 17, 2)])
+@pytest.mark.parametrize("scale", [np.inf, -np.inf, np.nan])
+def test_router_slots_without_an_expert_weigh_nothing(dev, score, e, topk, groups, keep, scale):
+    """Rows with 0, 1, ... experts on, under a factor that is no number."""
+    lg = np.full((topk + 2, e), -np.inf, np.float32)
+    for i in range(topk + 2):
+        lg[i, :i] = np.arange(i) / 8
+    lg[topk + 1, :topk] = np.nan
+    for renorm in (False, True):
+        ids, w = _ops().moe_router_scored(torch.from_numpy(lg).to(dev), topk, score=score,
+                                          n_groups=groups, topk_groups=keep, renormalize=renorm,
+                                          scale=scale)
+        ri, rw = O.router_scored(lg, topk, score, None, groups, keep, renorm, scale)
+        assert np.array_equal(ids.cpu().numpy(), ri) and (ri < 0).any()
+        assert np.array_equal(w.cpu().numpy(), rw.astype(np.float32), equal_nan=True)
+        assert (rw[ri < 0] == 0).all()
+    low = torch.full((3, e), -800.0, device=dev)     # sigmoid scores of 0: nothing to divide by
+    ids, w = _ops().moe_router_scored(low, topk, score="sigmoid", n_groups=groups,
+                                      topk_groups=keep, renormalize=True, scale=scale)
+    assert (ids >= 0).all() and (w == 0).all()
