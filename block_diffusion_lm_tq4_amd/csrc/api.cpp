@@ -958,7 +958,7 @@ int tq4_moe_router(const float *logits, int64_t t, int32_t n_experts, int32_t to
                    int32_t *topk_ids, float *topk_w, void *stream) {
   if (t < 0 || n_experts < 1 || n_experts > 512 || topk < 1 || topk > n_experts)
     return TQ4_E_SHAPE;
-  if (t > (int64_t{1} << 33)) return TQ4_E_SHAPE;  // grid of t / 4 workgroups
+  if (t > (int64_t{1} << 33)) return TQ4_E_SHAPE;  // 256 launches
   if (t == 0) return TQ4_OK;
   if (logits == nullptr || topk_ids == nullptr || topk_w == nullptr) return TQ4_E_NULL;
   if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4)) return TQ4_E_ALIGN;

@@ -631,14 +631,8 @@ __global__ __launch_bounds__(64 * kFastWaves) void router_fast_kernel(
   }
 }
 
-}  // namespace
-
-hipError_t launch_router_scored(const float *logits, int64_t t, const RouterConfig &config,
-                                const float *bias, int32_t *ids, float *w, hipStream_t s) {
-  if (t == 0) return hipSuccess;
-  RouterConfig cfg = config;
-  const int32_t per = cfg.n_experts / cfg.n_groups;
-  cfg.per_inv = static_cast<uint32_t>(((1 << 20) + per - 1) / per);
+hipError_t launch_some(const float *logits, int64_t t, const RouterConfig &cfg, const float *bias,
+                       int32_t *ids, float *w, hipStream_t s) {
   if (cfg.topk > kFastSlots || cfg.n_groups > kFastGroups) {
     hipLaunchKernelGGL(router_f64_kernel, dim3(static_cast<unsigned>((t + 3) / 4)), dim3(256), 0,
                        s, logits, t, cfg, bias, ids, w);
@@ -658,6 +652,22 @@ hipError_t launch_router_scored(const float *logits, int64_t t, const RouterConf
     hipLaunchKernelGGL(router_fast_kernel<32>, grid, block, 0, s, logits, t, cfg, bias, ids,
                        w);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_router_scored(const float *logits, int64_t t, const RouterConfig &config,
+                                const float *bias, int32_t *ids, float *w, hipStream_t s) {
+  RouterConfig cfg = config;
+  const int32_t per = cfg.n_experts / cfg.n_groups;
+  cfg.per_inv = static_cast<uint32_t>(((1 << 20) + per - 1) / per);
+  for (int64_t at = 0; at < t; at += kRouterLaunchTokens) {
+    const int64_t n = t - at < kRouterLaunchTokens ? t - at : kRouterLaunchTokens;
+    const hipError_t e = launch_some(logits + at * cfg.n_experts, n, cfg, bias,
+                                     ids + at * cfg.topk, w + at * cfg.topk, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace tq4

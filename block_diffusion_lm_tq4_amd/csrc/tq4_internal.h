@@ -375,6 +375,10 @@ hipError_t launch_read_probe(const void *src, int64_t bytes, float *sink, hipStr
 hipError_t launch_router(const float *logits, int64_t t, int32_t n_experts, int32_t topk,
                          int32_t *ids, float *gates, hipStream_t s);
 
+// A launch counts its threads in 32 bits.  Up to 64 of them route a token, so
+// the routers take more tokens than this in several launches.
+constexpr int64_t kRouterLaunchTokens = int64_t{1} << 25;
+
 // The scored router (router.hip).
 struct RouterConfig {
   int32_t n_experts, topk;

@@ -61,3 +61,20 @@ def test_router_slots_without_an_expert_weigh_nothing(dev, score, e, topk, group
     ids, w = _ops().moe_router_scored(low, topk, score="sigmoid", n_groups=groups,
                                       topk_groups=keep, renormalize=True, scale=scale)
     assert (ids >= 0).all() and (w == 0).all()
+
+
+def _repeat(rows, t):
+    """The given rows over and over, t in all."""
+    return rows.repeat((t + len(rows) - 1) // len(rows), 1)[:t]
+
+
+# past 2^32 threads at 16 and at 64 threads a token
+@pytest.mark.parametrize("t,e,topk,groups,keep", [(2 ** 28 + 21, 2, 1, 1, 1),
+                                                  (2 ** 26 + 13, 17, 2, 17, 2)])
+def test_router_of_more_tokens_than_a_launch_holds(dev, t, e, topk, groups, keep):
+    lg = np.random.default_rng(e).standard_normal((997, e)).astype(np.float32)
+    base, base_w = _check_router(dev, lg, topk, score="sigmoid", n_groups=groups,
+                                 topk_groups=keep)
+    ids, w = _ops().moe_router_scored(_repeat(torch.from_numpy(lg).to(dev), t), topk,
+                                      score="sigmoid", n_groups=groups, topk_groups=keep)
+    assert torch.equal(ids, _repeat(base, t)) and torch.equal(w, _repeat(base_w, t))
