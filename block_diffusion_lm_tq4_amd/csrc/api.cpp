@@ -923,7 +923,7 @@ int tq4_moe_router_scored(const float *logits, int64_t t, int32_t n_experts, int
                           void *stream) {
   if (t < 0 || n_experts < 1 || n_experts > 512 || topk < 1 || topk > n_experts)
     return TQ4_E_SHAPE;
-  if (t > (int64_t{1} << 33)) return TQ4_E_SHAPE;  // grid of t / 4 workgroups
+  if (t > (int64_t{1} << 33)) return TQ4_E_SHAPE;  // 256 launches
   if (score != TQ4_SCORE_SOFTMAX && score != TQ4_SCORE_SIGMOID) return TQ4_E_SHAPE;
   if (n_groups < 1 || n_experts % n_groups != 0 || topk_groups < 1 || topk_groups > n_groups)
     return TQ4_E_SHAPE;

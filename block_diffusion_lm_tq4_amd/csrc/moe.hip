@@ -227,10 +227,15 @@ hipError_t launch_combine(const float *o, const int32_t *inv, const float *topk_
 hipError_t launch_router(const float *logits, int64_t t, int32_t n_experts, int32_t topk,
                          int32_t *ids, float *gates, hipStream_t s) {
   if (n_experts > kMaxExperts) return hipErrorInvalidValue;
-  if (t == 0) return hipSuccess;
-  hipLaunchKernelGGL(router_kernel, dim3(static_cast<unsigned>((t + 3) / 4)), dim3(256), 0, s,
-                     logits, t, n_experts, topk, ids, gates);
-  return hipGetLastError();
+  for (int64_t at = 0; at < t; at += kRouterLaunchTokens) {
+    const int64_t n = t - at < kRouterLaunchTokens ? t - at : kRouterLaunchTokens;
+    hipLaunchKernelGGL(router_kernel, dim3(static_cast<unsigned>((n + 3) / 4)), dim3(256), 0, s,
+                       logits + at * n_experts, n, n_experts, topk, ids + at * topk,
+                       gates + at * topk);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace tq4

@@ -78,3 +78,13 @@ def test_router_of_more_tokens_than_a_launch_holds(dev, t, e, topk, groups, keep
     ids, w = _ops().moe_router_scored(_repeat(torch.from_numpy(lg).to(dev), t), topk,
                                       score="sigmoid", n_groups=groups, topk_groups=keep)
     assert torch.equal(ids, _repeat(base, t)) and torch.equal(w, _repeat(base_w, t))
+
+
+def test_softmax_router_of_more_tokens_than_a_launch_holds(dev):
+    t, e, topk = 2 ** 26 + 13, 3, 2
+    lg = torch.from_numpy(np.random.default_rng(1).standard_normal((997, e)).astype(np.float32))
+    base, base_w = _ops().moe_router(lg.to(dev), topk)
+    ri, rw = O.router_scored(lg.numpy(), topk)
+    assert np.array_equal(base.cpu().numpy(), ri) and np.allclose(base_w.cpu().numpy(), rw, 1e-5)
+    ids, w = _ops().moe_router(_repeat(lg.to(dev), t), topk)
+    assert torch.equal(ids, _repeat(base, t)) and torch.equal(w, _repeat(base_w, t))
