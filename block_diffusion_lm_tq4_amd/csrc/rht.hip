@@ -56,18 +56,31 @@ __global__ __launch_bounds__(256) void act_sign_kernel(const uint16_t *__restric
   }
 }
 
-__global__ __launch_bounds__(256) void fill_zero_kernel(float *__restrict__ p, int64_t count) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i < count) p[i] = 0.f;
+// The outputs of a product with an empty k.  A launch counts its threads in 32
+// bits and an output may have more elements, so the grid is bounded and walks.
+constexpr int64_t kFillThreads = 256;
+
+dim3 fill_grid(int64_t count) {
+  const int64_t groups = (count + kFillThreads - 1) / kFillThreads;
+  return dim3(static_cast<unsigned>(groups < (1 << 20) ? groups : (1 << 20)));
 }
 
-// y = bias + residual, for a product with an empty k.
-__global__ __launch_bounds__(256) void tail_only_kernel(Tail t, int64_t m, int64_t n, float *y) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= m * n) return;
-  const int64_t col = t.bias != nullptr ? i % n : 0;  // the column only feeds the bias
-  const float res = t.residual != nullptr ? tail_residual(t, i) : 0.f;
-  tail_store(t, y, i, tail_sum(t, 0.f, col, res));
+__global__ __launch_bounds__(kFillThreads) void fill_zero_kernel(float *__restrict__ p,
+                                                                 int64_t count) {
+  for (int64_t i = blockIdx.x * kFillThreads + threadIdx.x; i < count;
+       i += gridDim.x * kFillThreads)
+    p[i] = 0.f;
+}
+
+// y = bias + residual.
+__global__ __launch_bounds__(kFillThreads) void tail_only_kernel(Tail t, int64_t m, int64_t n,
+                                                                 float *y) {
+  for (int64_t i = blockIdx.x * kFillThreads + threadIdx.x; i < m * n;
+       i += gridDim.x * kFillThreads) {
+    const int64_t col = t.bias != nullptr ? i % n : 0;  // the column only feeds the bias
+    const float res = t.residual != nullptr ? tail_residual(t, i) : 0.f;
+    tail_store(t, y, i, tail_sum(t, 0.f, col, res));
+  }
 }
 
 }  // namespace
@@ -75,15 +88,13 @@ __global__ __launch_bounds__(256) void tail_only_kernel(Tail t, int64_t m, int64
 hipError_t launch_tail_only(const Tail &t, int64_t m, int64_t n, float *y, hipStream_t s) {
   const int64_t count = m * n;
   if (count == 0) return hipSuccess;
-  hipLaunchKernelGGL(tail_only_kernel, dim3(static_cast<unsigned>((count + 255) / 256)), dim3(256),
-                     0, s, t, m, n, y);
+  hipLaunchKernelGGL(tail_only_kernel, fill_grid(count), dim3(kFillThreads), 0, s, t, m, n, y);
   return hipGetLastError();
 }
 
 hipError_t launch_fill_zero(float *p, int64_t count, hipStream_t s) {
   if (count == 0) return hipSuccess;
-  hipLaunchKernelGGL(fill_zero_kernel, dim3(static_cast<unsigned>((count + 255) / 256)), dim3(256),
-                     0, s, p, count);
+  hipLaunchKernelGGL(fill_zero_kernel, fill_grid(count), dim3(kFillThreads), 0, s, p, count);
   return hipGetLastError();
 }
 
