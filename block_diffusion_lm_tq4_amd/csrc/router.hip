@@ -4,7 +4,8 @@
 // which the best are kept, and weights that may be renormalized and scaled.
 //
 // Per token, with scores p_e and choice values c_e = p_e + bias_e:
-//   - an expert whose logit is -inf or NaN, or whose c is, is never chosen;
+//   - an expert whose logit is -inf or NaN takes no part; one whose bias is only
+//     cannot be chosen (its score still counts in the others' softmax);
 //   - with groups, a group's value is the sum of its two largest c (of the
 //     one, if only one may be chosen); the keep groups with the largest values
 //     stay (ties to the lower group);

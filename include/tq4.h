@@ -511,9 +511,11 @@ int tq4_moe_router(const float *logits, int64_t t, int32_t n_experts, int32_t to
  *   topk_w[t, j] = scale * p[topk_ids[t, j]], divided by the sum of the
  *           token's chosen p if renormalize is not zero (0 if that sum is 0).
  * Scores, comparisons and weights are fp64, the weights then rounded to fp32.
- * An expert whose logit is -infinity or NaN, or whose c is, is switched off:
- * it takes no part in the softmax and is never chosen; +infinity counts as
- * the largest finite value.  A group without an expert left is never kept.
+ * An expert whose logit is -infinity or NaN is switched off: it takes no part
+ * in the softmax and is never chosen.  A bias of -infinity or NaN only bars the
+ * choice: such an expert is never chosen either, and its logit stays in the
+ * softmax of the others.  A logit of +infinity counts as the largest finite
+ * value.  A group without an expert left is never kept.
  * Slots for which no expert is left get id -1 and weight 0, which the MoE
  * layers above skip.
  *   logits   : [t, n_experts] fp32, device

@@ -14,8 +14,9 @@ every forward runs; *The model underneath*: 128 experts, top-6):
 * y[m, n] = (sum_k xq wq) * sx[m] * sw[n], the sum exact;
 * the MoE layer keeps its hidden rows relu(u)^2 in bf16 (rounded from fp32) and
   quantizes them like the activations;
-* the router: softmax or sigmoid scores, a bias that only the choice sees,
-  groups valued by their two best experts, ties to the lower index, weights
+* the router: softmax or sigmoid scores over the experts whose logit is a number
+  above -inf, a bias that only the choice sees (-inf or NaN: never chosen), groups
+  valued by their two best experts, ties to the lower index, weights
   renormalized and scaled.
 """
 

@@ -88,3 +88,25 @@ def test_softmax_router_of_more_tokens_than_a_launch_holds(dev):
     assert np.array_equal(base.cpu().numpy(), ri) and np.allclose(base_w.cpu().numpy(), rw, 1e-5)
     ids, w = _ops().moe_router(_repeat(lg.to(dev), t), topk)
     assert torch.equal(ids, _repeat(base, t)) and torch.equal(w, _repeat(base_w, t))
+
+
+# by the fp32 choice, by its fp64 pass (a bias of +inf), by the wave a token
+@pytest.mark.parametrize("case", ["fast", "again", "wave"])
+@pytest.mark.parametrize("barred", [-np.inf, np.nan])
+def test_router_bias_that_bars_leaves_the_softmax_alone(dev, barred, case):
+    """exp(l) = 1, 2, 4, 1 over and over, 64 in all over 32 experts.  The fours are
+    barred but keep their share, so that weights are 2 / 64 and 1 / 64."""
+    e, topk = 32, 16 if case == "wave" else 10
+    lg = torch.log(torch.tensor([1.0, 2.0, 4.0, 1.0], dtype=torch.float64)).float().to(dev)
+    bias = torch.zeros(e)
+    bias[2::4] = barred
+    if case == "again":
+        bias[5] = np.inf
+    ids, w = _ops().moe_router_scored(lg.repeat(5, e // 4), topk, bias=bias.to(dev))
+    two, one = list(range(1, 32, 4)), sorted([*range(0, 32, 4), *range(3, 32, 4)])
+    order = [5] + [x for x in two if x != 5] if case == "again" else two
+    assert ids.cpu().tolist() == [(order + one)[:topk]] * 5
+    ref = torch.tensor([2 / 64] * 8 + [1 / 64] * (topk - 8), dtype=torch.float64)
+    # log 2 and log 4 are off by 2^-25 and 2^-24, their shares of the sum make 0.63 *
+    # 2^-24 of that, and the weight is rounded: 2.2 * 2^-24
+    assert ((w.cpu().double() - ref).abs() <= 3 * 2.0 ** -24 * ref).all()
