@@ -820,8 +820,9 @@ __global__ __launch_bounds__(128 * kDirectSlots) void i8_direct_down_kernel(I8Ar
 // A wave's MS x NS sub-tiles to memory through LDS.  Straight from the product's
 // layout a store instruction would write 16 rows x 64 bytes (32 for bf16),
 // half a cache line each; instead 16 rows at a time go to a wave's own LDS
-// buffer (two in turn, rows 16 bytes longer than their data, so that neither
-// the writes nor the reads share banks) and come back as whole row segments
+// buffer (two in turn, so that a group's reads are behind the next one's fence
+// before they are overwritten; rows 16 bytes longer than their data, so that
+// neither the writes nor the reads share banks) and come back as whole row segments
 // of 16 * NS outputs.  Stores are non-temporal: nothing reads the output before
 // the operands that it would push out of the caches are needed (4096 x 2688 x
 // 8192: 107 -> 96 us, the up product of 1024 tokens on 128 experts 134.5 -> 124).
@@ -922,6 +923,7 @@ __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], u
       for (int j = 0; j < NS; ++j)
         *reinterpret_cast<uint2 *>(buf + r * kRowBytes + 32 * j + 8 * grp) =
             hidden_quad(acc[i][j], sx[i], sw[j], tame);
+      wave_lds_fence();
 #pragma unroll
       for (int q = 0; q < kReads; ++q) {
         const int f = 512 * q + 8 * lane;
@@ -947,6 +949,7 @@ __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], u
       for (int v = 0; v < 4; ++v) p[v] = (static_cast<float>(acc[i][j][v]) * sx[i]) * sw[j][v];
       *reinterpret_cast<floatx4 *>(buf + r * kStride + 16 * j + 4 * grp) = p;
     }
+    wave_lds_fence();
     float val[kGroups][E];
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
