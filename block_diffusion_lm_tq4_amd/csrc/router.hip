@@ -132,12 +132,12 @@ __device__ inline void wave_lds_fence() {
 // first: a sum below 2^-1022, as of experts that only their bias brought in, has
 // no finite reciprocal.
 __device__ inline float weight(bool found, double p, double total, const RouterConfig &cfg) {
-  if (!found) return 0.f;
   if (cfg.renormalize) {
-    if (!(total > 0.0)) return 0.f;
+    found = found && total > 0.0;
     p /= total;
   }
-  return static_cast<float>(p * static_cast<double>(cfg.scale));
+  const float w = static_cast<float>(p * static_cast<double>(cfg.scale));
+  return found ? w : 0.f;
 }
 
 // Writes the token's ids[0 .. topk) and w[0 .. topk); gv: kMaxExperts doubles of
