@@ -511,6 +511,9 @@ int tq4_moe_router(const float *logits, int64_t t, int32_t n_experts, int32_t to
  *   topk_w[t, j] = scale * p[topk_ids[t, j]], divided by the sum of the
  *           token's chosen p if renormalize is not zero (0 if that sum is 0).
  * Scores, comparisons and weights are fp64, the weights then rounded to fp32.
+ * The time depends on the values: fp32 decides most choices, and a token that it
+ * does not settle is done again in fp64.  Where all are (equal logits, sigmoid
+ * logits of 10 and more, both without a bias) a call takes up to 6 times as long.
  * An expert whose logit is -infinity or NaN is switched off: it takes no part
  * in the softmax and is never chosen.  A bias of -infinity or NaN only bars the
  * choice: such an expert is never chosen either, and its logit stays in the
