@@ -635,11 +635,11 @@ __global__ __launch_bounds__(64 * KW) void i8_skinny_kernel(I8Args g) {
 // a call); 8192 x 2688 7.7 against 10.8.  From two rows on the wave's own quantization costs more than it
 // saves (10.2 against 9.1 us).
 
-constexpr int kDirectVecs = 16;   // pieces of 8 values per lane: k <= 8192
 constexpr int kDirectSteps = 16;  // steps of 64 k per wave
 
-// A wave's row: request(), then other loads, then finish(), which leaves the
-// codes of steps [s0, s1) in `codes` and returns what the row's maximum says.
+// A wave's row, V pieces of 8 values per lane: request(), then other loads, then
+// finish(), which leaves the codes of steps [s0, s1) in `codes` and returns what the
+// row's maximum says.
 template <int V>
 struct DirectRow {
   uint4 all[V], own[2];
@@ -1401,20 +1401,23 @@ int direct_steps(int64_t k, int waves) {
   return static_cast<int>((steps + waves - 1) / waves);
 }
 
+// Pieces of 8 values that a lane holds of the longest row whose steps `waves` share.
+constexpr int direct_vecs(int waves) { return waves * kDirectSteps * kI8Step / (64 * 8); }
+
 template <int MODE, int KW, int B>
 hipError_t launch_direct(const I8Args &g, const I8Direct &d, dim3 grid, hipStream_t s) {
   if (d.k <= 64 * 8 * 6)
     hipLaunchKernelGGL((i8_direct_kernel<MODE, KW, B, 6>), grid, dim3(64 * KW), 0, s, g, d);
   else
-    hipLaunchKernelGGL((i8_direct_kernel<MODE, KW, B, kDirectVecs>), grid, dim3(64 * KW), 0, s, g,
-                       d);
+    hipLaunchKernelGGL((i8_direct_kernel<MODE, KW, B, direct_vecs(KW)>), grid, dim3(64 * KW), 0, s,
+                       g, d);
   return hipGetLastError();
 }
 
 }  // namespace
 
 bool int8_direct_fits(int64_t m, int64_t k) {
-  return m == 1 && k <= 64 * 8 * kDirectVecs && direct_steps(k, 8) <= kDirectSteps;
+  return m == 1 && direct_steps(k, 8) <= kDirectSteps;
 }
 
 hipError_t launch_linear_int8_direct(const uint16_t *x, int64_t m, int64_t k, const int8_t *wq,
@@ -1445,8 +1448,8 @@ hipError_t launch_linear_int8_direct(const uint16_t *x, int64_t m, int64_t k, co
 // the batched steps, two 37 against 42, four 65 against 62 (the batched steps
 // read an expert that two tokens share once).
 bool int8_moe_direct_fits(int64_t t, int32_t topk, int64_t n1, int64_t k) {
-  return t * topk <= 12 && topk <= kDirectSlots && k <= 64 * 8 * kDirectVecs &&
-         direct_steps(k, 4) <= kDirectSteps && direct_steps(n1, 2) <= kDirectSteps;
+  return t * topk <= 12 && topk <= kDirectSlots && direct_steps(k, 4) <= kDirectSteps &&
+         direct_steps(n1, 2) <= kDirectSteps;
 }
 
 hipError_t launch_moe_int8_direct(const uint16_t *x, int64_t t, int64_t k, const int32_t *ids,
@@ -1479,8 +1482,7 @@ hipError_t launch_moe_int8_direct(const uint16_t *x, int64_t t, int64_t k, const
   d.x = h;
   d.k = static_cast<int32_t>(n1);
   const dim3 grid2(static_cast<unsigned>((k + 15) / 16), static_cast<unsigned>(t));
-  // two halves of at most 16 steps: rows of at most 2048 values
-  hipLaunchKernelGGL((i8_direct_down_kernel<kDirectSteps, 4>), grid2,
+  hipLaunchKernelGGL((i8_direct_down_kernel<kDirectSteps, direct_vecs(2)>), grid2,
                      dim3(static_cast<unsigned>(128 * topk)), 0, s, g, d);
   return hipGetLastError();
 }
