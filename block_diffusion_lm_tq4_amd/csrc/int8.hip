@@ -432,60 +432,46 @@ __device__ inline void store_dense(const I8Args &g, int64_t at, int left, const 
   }
 }
 
-// A wave's MS x NS sub-tiles of a dense output: row m0 + 16 i + lane % 16,
-// columns n0 + 16 j + 4 (lane / 16) ...; `rows` valid rows from m0.
-template <int MS, int NS, bool BF16, bool VEC>
-__device__ inline void store_block(const I8Args &g, const intx4 (&acc)[MS][NS], int64_t m0,
-                                   int rows, int64_t n0, const float (&sx)[MS], int lane) {
+// A wave's 16 x 16 block of a dense output: row lane % 16 of `rows` valid ones,
+// columns n0 + 4 (lane / 16) ....
+template <bool BF16, bool VEC>
+__device__ inline void store_block(const I8Args &g, intx4 acc, int rows, int64_t n0, float sx,
+                                   int lane) {
 #pragma clang fp contract(off)
   const int r = lane % 16;
+  const int64_t n = n0 + 4 * (lane / 16);
+  const int left = g.n - n < 4 ? static_cast<int>(g.n - n) : 4;
+  if (r >= rows || left <= 0) return;
   const bool has_bias = g.tail.bias != nullptr;
   const bool has_res = g.tail.residual != nullptr;
+  float sw[4], bias[4], res[4], p[4];
 #pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    const int64_t n = n0 + 16 * j + 4 * (lane / 16);
-    const int left = g.n - n < 4 ? static_cast<int>(g.n - n) : 4;
-    if (left <= 0) continue;
-    float sw[4], bias[4];
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      sw[v] = v < left ? g.ws[n + v] : 0.f;
-      bias[v] = has_bias && v < left ? g.tail.bias[n + v] : 0.f;
-    }
-    float res[MS][4];
-    if (has_res) {
-#pragma unroll
-      for (int i = 0; i < MS; ++i)
-        if (16 * i + r < rows)
-          load_residual<BF16, VEC>(g, (m0 + 16 * i + r) * g.n + n, left, res[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < MS; ++i) {
-      float p[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        p[v] = (static_cast<float>(acc[i][j][v]) * sx[i]) * sw[v];
-        if (has_bias) p[v] += bias[v];
-        if (has_res) p[v] += res[i][v];
-      }
-      if (16 * i + r < rows) store_dense<BF16, VEC>(g, (m0 + 16 * i + r) * g.n + n, left, p);
-    }
+  for (int v = 0; v < 4; ++v) {
+    sw[v] = v < left ? g.ws[n + v] : 0.f;
+    bias[v] = has_bias && v < left ? g.tail.bias[n + v] : 0.f;
   }
+  if (has_res) load_residual<BF16, VEC>(g, r * g.n + n, left, res);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    p[v] = (static_cast<float>(acc[v]) * sx) * sw[v];
+    if (has_bias) p[v] += bias[v];
+    if (has_res) p[v] += res[v];
+  }
+  store_dense<BF16, VEC>(g, r * g.n + n, left, p);
 }
 
-template <int MS, int NS>
-__device__ inline void store_any(const I8Args &g, const intx4 (&acc)[MS][NS], int64_t m0,
-                                 int rows, int64_t n0, const float (&sx)[MS], int lane) {
+__device__ inline void store_any(const I8Args &g, intx4 acc, int rows, int64_t n0, float sx,
+                                 int lane) {
   if (g.vec) {
     if (g.tail.bf16)
-      store_block<MS, NS, true, true>(g, acc, m0, rows, n0, sx, lane);
+      store_block<true, true>(g, acc, rows, n0, sx, lane);
     else
-      store_block<MS, NS, false, true>(g, acc, m0, rows, n0, sx, lane);
+      store_block<false, true>(g, acc, rows, n0, sx, lane);
   } else {
     if (g.tail.bf16)
-      store_block<MS, NS, true, false>(g, acc, m0, rows, n0, sx, lane);
+      store_block<true, false>(g, acc, rows, n0, sx, lane);
     else
-      store_block<MS, NS, false, false>(g, acc, m0, rows, n0, sx, lane);
+      store_block<false, false>(g, acc, rows, n0, sx, lane);
   }
 }
 
@@ -504,16 +490,16 @@ __device__ inline void load_sw(const I8Args &g, int64_t w0, int64_t n, float (&s
 }
 
 // ---- few rows ---------------------------------------------------------------
-// Up to 16 * MT rows: the weights are read once, straight into registers, and
-// the product is bound by that stream.  A workgroup of KW waves takes 16 * NT
-// columns; wave w takes the 64-k steps [w * per, (w + 1) * per) of them, B at
-// a time, all loads of a batch issued before its first product.  The waves'
-// int32 sums meet in LDS (exact in any order).  16 tokens on 128 experts of
-// 1856 x 2688: up 62 us, down 57 for 357 MB each, 5.6 to 5.8 TB/s.
-template <int MODE, int MT, int NT, int KW, int B>
+// Up to 16 rows: the weights are read once, straight into registers, and the
+// product is bound by that stream.  A workgroup of KW waves takes 16 columns; wave
+// w takes the 64-k steps [w * per, (w + 1) * per) of them, B at a time, all loads
+// of a batch issued before its first product.  The waves' int32 sums meet in LDS
+// (exact in any order).  16 tokens on 128 experts of 1856 x 2688: up 62 us, down 57
+// for 357 MB each, 5.6 to 5.8 TB/s.
+template <int MODE, int KW, int B>
 __global__ __launch_bounds__(64 * KW) void i8_skinny_kernel(I8Args g) {
   static_assert(KW > 1, "the waves share k");
-  __shared__ intx4 red[KW - 1][MT][NT][64];
+  __shared__ intx4 red[KW - 1][64];
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int lane = tid % 64;
@@ -523,7 +509,7 @@ __global__ __launch_bounds__(64 * KW) void i8_skinny_kernel(I8Args g) {
   int64_t n0, m0 = 0, w0 = 0;
   int rows;
   if constexpr (MODE == kI8Dense) {
-    n0 = static_cast<int64_t>(blockIdx.x) * (16 * NT);
+    n0 = static_cast<int64_t>(blockIdx.x) * 16;
     rows = static_cast<int>(g.m);
   } else {
     // column blocks are dealt to the XCDs (workgroup id % 8), rotated by the
@@ -536,87 +522,48 @@ __global__ __launch_bounds__(64 * KW) void i8_skinny_kernel(I8Args g) {
     const MoETile t = g.tiles[i];
     const int j = (static_cast<int>(blockIdx.x) + t.expert) % 8 + 8 * (q % per);
     if (j >= g.tiles_n) return;
-    n0 = static_cast<int64_t>(j) * (16 * NT);
+    n0 = static_cast<int64_t>(j) * 16;
     m0 = t.row0;
     rows = t.rows;
     w0 = static_cast<int64_t>(t.expert) * g.n;
   }
 
-  const int8_t *wp[NT];
-  const int8_t *xp[MT];
-  int64_t src[MT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t n = n0 + 16 * j + r;
-    wp[j] = g.wq + (w0 + (n < g.n ? n : g.n - 1)) * g.kp + 16 * grp;  // past n: read n - 1
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = m0 + (16 * i + r < rows ? 16 * i + r : 0);  // past the rows: the first
-    src[i] = MODE == kI8Up ? g.perm[m] / g.topk : m;
-    xp[i] = g.xq + src[i] * g.kp + 16 * grp;
-  }
-  intx4 acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = intx4{0, 0, 0, 0};
+  const int64_t nr = n0 + r < g.n ? n0 + r : g.n - 1;  // past n: read n - 1
+  const int8_t *wp = g.wq + (w0 + nr) * g.kp + 16 * grp;
+  const int64_t mr = m0 + (r < rows ? r : 0);          // past the rows: the first
+  const int64_t src = MODE == kI8Up ? g.perm[mr] / g.topk : mr;
+  const int8_t *xp = g.xq + src * g.kp + 16 * grp;
+  intx4 acc = {0, 0, 0, 0};
 
   const int steps = g.kp / kI8Step;
   const int per = (steps + KW - 1) / KW;
   const int s0 = wave * per;
   const int s1 = s0 + per < steps ? s0 + per : steps;
   for (int s = s0; s < s1; s += B) {
-    intx4 a[B][NT], b[B][MT];
+    intx4 a[B], b[B];
 #pragma unroll
     for (int u = 0; u < B; ++u) {
       // steps past the wave's end reload its last one and are not multiplied
       const int64_t k0 = static_cast<int64_t>(s + u < s1 ? s + u : s1 - 1) * kI8Step;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) a[u][j] = *reinterpret_cast<const intx4 *>(wp[j] + k0);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) b[u][i] = *reinterpret_cast<const intx4 *>(xp[i] + k0);
+      a[u] = *reinterpret_cast<const intx4 *>(wp + k0);
+      b[u] = *reinterpret_cast<const intx4 *>(xp + k0);
     }
 #pragma unroll
-    for (int u = 0; u < B; ++u) {
-      if (s + u < s1) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][j], b[u][i], acc[i][j], 0, 0, 0);
-      }
-    }
+    for (int u = 0; u < B; ++u)
+      if (s + u < s1) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], b[u], acc, 0, 0, 0);
   }
-  if (wave > 0) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) red[wave - 1][i][j][lane] = acc[i][j];
-  }
+  if (wave > 0) red[wave - 1][lane] = acc;
   __syncthreads();
   if (wave > 0) return;  // wave 0 adds the others' sums and stores
 #pragma unroll
-  for (int w = 0; w < KW - 1; ++w)
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] += red[w][i][j][lane];
+  for (int w = 0; w < KW - 1; ++w) acc += red[w][lane];
+  const float sx = g.xs[src];
   if constexpr (MODE == kI8Dense) {
-    float sx[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) sx[i] = g.xs[src[i]];
-    store_any<MT, NT>(g, acc, m0, rows, n0, sx, lane);
-  } else {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      float sw[4];
-      load_sw(g, w0, n0 + 16 * j + 4 * grp, sw);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        if (16 * i + r < rows)
-          store_moe<MODE>(g, acc[i][j], m0 + 16 * i + r, n0 + 16 * j + 4 * grp, g.xs[src[i]], sw);
-    }
+    store_any(g, acc, rows, n0, sx, lane);
+  } else if (r < rows) {
+    float sw[4];
+    load_sw(g, w0, n0 + 4 * grp, sw);
+    store_moe<MODE>(g, acc, m0 + r, n0 + 4 * grp, sx, sw);
   }
 }
 
@@ -756,9 +703,7 @@ __global__ __launch_bounds__(64 * KW) void i8_direct_kernel(I8Args g, I8Direct d
 #pragma unroll
   for (int w = 0; w < KW - 1; ++w) acc += red[w][lane];
   if constexpr (MODE == kI8Dense) {
-    const intx4 block[1][1] = {{acc}};
-    const float scale[1] = {rs.scale};
-    store_any<1, 1>(g, block, 0, 1, n0, scale, lane);
+    store_any(g, acc, 1, n0, rs.scale, lane);
   } else if (r == 0) {
     float sw[4];
     load_sw(g, w0, n0 + 4 * grp, sw);
@@ -1274,13 +1219,13 @@ hipError_t launch_tile(I8Args g, int64_t max_tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int MODE, int MT, int NT, int KW, int B>
+template <int MODE, int KW, int B>
 hipError_t launch_skinny_cfg(I8Args g, int64_t max_tiles, hipStream_t s) {
-  g.tiles_n = static_cast<int32_t>((g.n + 16 * NT - 1) / (16 * NT));
+  g.tiles_n = static_cast<int32_t>((g.n + 15) / 16);
   const int64_t grid =
       MODE == kI8Dense ? g.tiles_n : max_tiles * ((g.tiles_n + 7) / 8 * 8);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((i8_skinny_kernel<MODE, MT, NT, KW, B>), dim3(static_cast<unsigned>(grid)),
+  hipLaunchKernelGGL((i8_skinny_kernel<MODE, KW, B>), dim3(static_cast<unsigned>(grid)),
                      dim3(64 * KW), 0, s, g);
   return hipGetLastError();
 }
@@ -1513,8 +1458,8 @@ hipError_t launch_linear_int8(const int8_t *xq, const float *xs, int64_t m, int6
   // (k = 8192, n = 2688: 10.4 us in sixes, 9.7 in eights; k = 2688, n = 8192
   // the other way round, 7.4 and 8.9).
   if (m <= 16 && n <= 4096) {
-    if (halves <= 8 * 6) return launch_skinny_cfg<kI8Dense, 1, 1, 8, 6>(g, 0, s);
-    return launch_skinny_cfg<kI8Dense, 1, 1, 8, 8>(g, 0, s);
+    if (halves <= 8 * 6) return launch_skinny_cfg<kI8Dense, 8, 6>(g, 0, s);
+    return launch_skinny_cfg<kI8Dense, 8, 8>(g, 0, s);
   }
   switch (pick_tile(m, n)) {
     case 0: return launch_tile<kI8Dense, 2, 2, 1, 1, 128, 5, 2>(g, 0, s);
@@ -1566,10 +1511,10 @@ hipError_t launch_moe_int8(int mode, int tile_rows, const int8_t *aq, const floa
   switch (tile_rows) {
     case 16:
       if (mode == 0)
-        return eights ? launch_skinny_cfg<kI8Up, 1, 1, 4, 8>(g, max_tiles, s)
-                      : launch_skinny_cfg<kI8Up, 1, 1, 4, 11>(g, max_tiles, s);
-      return eights ? launch_skinny_cfg<kI8Down, 1, 1, 4, 8>(g, max_tiles, s)
-                    : launch_skinny_cfg<kI8Down, 1, 1, 4, 11>(g, max_tiles, s);
+        return eights ? launch_skinny_cfg<kI8Up, 4, 8>(g, max_tiles, s)
+                      : launch_skinny_cfg<kI8Up, 4, 11>(g, max_tiles, s);
+      return eights ? launch_skinny_cfg<kI8Down, 4, 8>(g, max_tiles, s)
+                    : launch_skinny_cfg<kI8Down, 4, 11>(g, max_tiles, s);
     case 64:
       if (mode == 0) return launch_tile<kI8Up, 1, 4, 4, 2, 128, 3, 2>(g, max_tiles, s);
       return launch_tile<kI8Down, 1, 4, 4, 2, 128, 3, 2>(g, max_tiles, s);
