@@ -8,7 +8,7 @@
 
 #include "../../include/tq4.h"
 #include "moe_block.h"
-#include "tq4_internal.h"
+#include "int8_router.h"
 
 namespace {
 

@@ -28,7 +28,7 @@
 
 #include <type_traits>
 
-#include "tq4_internal.h"
+#include "int8_router.h"
 
 namespace tq4 {
 namespace {

@@ -6,7 +6,7 @@
 // Performance & why it's slow).  Everything below stays on the device: the
 // bucketing writes the expert counts, offsets, the stable permutation and the
 // tile list that the grouped products read, and the host never looks at them.
-#include "tq4_internal.h"
+#include "int8_router.h"
 
 namespace tq4 {
 namespace {

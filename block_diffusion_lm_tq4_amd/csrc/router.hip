@@ -20,7 +20,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "tq4_internal.h"
+#include "int8_router.h"
 
 namespace tq4 {
 namespace {
