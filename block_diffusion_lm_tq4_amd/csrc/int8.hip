@@ -41,13 +41,6 @@ constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / 64;
 #include "moe_route.h"
 
-// A wave's LDS writes before its later reads (nothing but the compiler could
-// change their order).
-__device__ inline void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // ---------------------------------------------------------------------------
 // Rows to codes
 

@@ -1,11 +1,18 @@
-// The launchers of the int8 products (int8.hip) and of the scored router
-// (router.hip), apart from tq4_internal.h: the committed traffic counters of the
+// What int8.hip (the int8 products) and router.hip (the scored router) share and
+// their launchers, apart from tq4_internal.h: the committed traffic counters of the
 // TQ4_1S kernels belong to that header's text, which these are no part of.
 #pragma once
 
 #include "tq4_internal.h"
 
 namespace tq4 {
+
+// A wave's LDS writes before its later reads, its own lanes' and the others'
+// (nothing but the compiler could change their order).
+__device__ inline void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 // int8 products (codes [rows][int8_padded_k(k)] with zero codes behind k, one
 // fp32 scale per row).

@@ -25,7 +25,8 @@
 namespace tq4 {
 namespace {
 
-constexpr int kMaxExperts = 512;
+#include "moe_route.h"
+
 constexpr int kPer = kMaxExperts / 64;
 constexpr double kNone = -__builtin_inf();
 constexpr float kNoneF = -__builtin_inff();
@@ -33,11 +34,6 @@ constexpr float kNoneF = -__builtin_inff();
 // ---- one token by one wave, all in fp64 -------------------------------------
 // Any number of groups and slots.  Lane l holds experts l, l + 64, ...
 
-template <int CTRL>
-__device__ inline float dpp_f(float v) {
-  return __builtin_bit_cast(
-      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
-}
 template <int CTRL>
 __device__ inline int dpp_i(int v) {
   return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, false);
@@ -119,12 +115,6 @@ __device__ inline void wave_best(double &v, int &i) {
   v = vl;
   i = static_cast<int>(il);
   better_f64(v, i, vh, static_cast<int>(ih));
-}
-
-// A wave's LDS writes before its later reads.
-__device__ inline void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-  __builtin_amdgcn_wave_barrier();
 }
 
 // A slot's weight from its expert's score p and the sum of the token's; 0 without
