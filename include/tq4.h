@@ -358,9 +358,10 @@ size_t tq4_linear_int8_workspace_size(int64_t m, int64_t k, int64_t n);
 
 /* y[m, n] = (sum_k xq[m, k] wq[n, k]) * sx[m] * sw[n]: x quantized per call
  * (tq4_act_int8, into the workspace), the weights from a cache built by
- * tq4_int8_cache or tq4_int8_cache_bf16.  The sum is exact, the two products
- * with the scales are fp32 in this order; deterministic.  (A sum times sx
- * past fp32's range is infinite, whatever sw.)  Rows of x that hold
+ * tq4_int8_cache or tq4_int8_cache_bf16.  The sum is exact; its rounding to
+ * fp32 and the two products with the scales are fp32 in this order;
+ * deterministic.  (A sum times sx past fp32's range is infinite, whatever sw.)
+ * Rows of x that hold
  * a NaN or an infinity, and such rows of the weights, give NaN.
  *   x_bf16 : [m, k] bf16 bit patterns, device, 16-byte aligned
  *   cache  : for this [n, k], device, 16-byte aligned
@@ -427,7 +428,8 @@ size_t tq4_moe_grouped_int8_workspace_size(int64_t t, int32_t topk, int32_t n_ex
  * of the hidden row * scale of W2's, fp32 in this order), and the per-token
  * weighted sum in slot order (fp32).  Deterministic.  Errors: as
  * tq4_moe_grouped, plus TQ4_E_SHAPE when t * kp or t * topk * n1p reach 2^31
- * (kp, n1p: k, n1 padded to 64) or k or n1 exceed 131072. */
+ * (kp, n1p: k, n1 padded to 64), when k or n1 exceed 131072, or when the pairs
+ * may need 65536 row tiles or more (t * topk / 256 + n_experts >= 65535). */
 int tq4_moe_grouped_int8(const uint16_t *x_bf16, int64_t t, int64_t k, const int32_t *topk_ids,
                          const float *topk_w, int32_t topk, int32_t n_experts,
                          const uint8_t *w1_cache, int64_t n1, const uint8_t *w2_cache, float *out,
