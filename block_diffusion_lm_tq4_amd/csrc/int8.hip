@@ -216,7 +216,8 @@ __global__ __launch_bounds__(kRouteThreads) void i8_route_act_kernel(
 // Packed TQ4_1S rows, one workgroup per row, in fp64: the butterfly's sums v
 // (sign undone) carry the row without its common factor 1/sqrt(32), which
 // leaves the codes' quotient; the scale takes it back in.  The row is decoded
-// twice, once for the maximum and once for the codes (offline work).
+// twice, once for the maximum and once for the codes (offline work): 237568 rows of
+// 2688 take 1.8 ms, 0.6 TB/s of what they read and write, bound by the fp64.
 __device__ inline bool decode_block(const uint32_t *p, uint32_t sign_bits, const Codebook &cb,
                                     double (&v)[32]) {
   uint32_t wd[5];
@@ -487,8 +488,9 @@ __device__ inline void load_sw(const I8Args &g, int64_t w0, int64_t n, float (&s
 // product is bound by that stream.  A workgroup of KW waves takes 16 columns; wave
 // w takes the 64-k steps [w * per, (w + 1) * per) of them, B at a time, all loads
 // of a batch issued before its first product.  The waves' int32 sums meet in LDS
-// (exact in any order).  16 tokens on 128 experts of 1856 x 2688: up 62 us, down 57
-// for 357 MB each, 5.6 to 5.8 TB/s.
+// (exact in any order).  16 tokens on 128 experts of 1856 x 2688 (median and range of
+// 60 calls): up 72 us (65 to 80), down 63 (61 to 67), for 357 MB each: 5.0 and 5.7
+// TB/s.
 template <int MODE, int KW, int B>
 __global__ __launch_bounds__(64 * KW) void i8_skinny_kernel(I8Args g) {
   static_assert(KW > 1, "the waves share k");
@@ -948,11 +950,15 @@ __device__ inline void store_rows(const I8Args &g, const intx4 (&acc)[MS][NS], u
 // banks.  Rows past the tile's end read zeros (dense; the buffer range ends
 // there) or the tile's first row (MoE) and are not stored.
 //
-// 4096 x 2688 x 8192 (256 x 256 tiles): 86 to 92 us, 2.0 to 2.1 POP/s, MFMA busy
-// 63 % at the 1.85 GHz that the power leaves; 4096 x 8192 x 2688 81 us.  MoE, 128
-// experts of 1856 x 2688, up / down: 1024 tokens 124 / 146 us, which is the weight
-// stream at 4.4 to 5.2 TB/s; 4096 tokens 190 / 219, of which the loop is 150 / 180
-// and the rest the hidden values and stores of one workgroup per compute unit.
+// Bound at many rows by MFMA at the clock that the power leaves.  4096 x 2688 x 8192
+// (256 x 256 tiles): 95 to 97 us captured (runs from 92 to 124), 1.9 POP/s; in a run
+// with counters (96.7 us) MFMA is busy in 53 % of the compute units' cycles, at 1.7
+// GHz.  4096 x 8192 x 2688: 90 us (85 to 117), MFMA busy 55 %.  One call after
+// another under a profiler: 112 (92 to 117) and 105 (90 to 119).  MoE, 128 experts
+// of 1856 x 2688, up / down, medians and ranges of 60 calls: 1024 tokens, popular
+// experts, 146 (142 to 156) / 165 (161 to 174) us, 5.4 and 5.3 TB/s; 4096 tokens 197
+// (188 to 240) / 230 (221 to 259), of which the loop is 150 / 180 and the rest the
+// hidden values and stores of one workgroup per compute unit; MFMA busy 38 / 30 %.
 template <int MODE, int WM, int WN, int MS, int NS, int KB, int S, int OCC, bool PP>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void i8_tile_kernel(I8Args g) {
   constexpr int W = WM * WN;
@@ -1300,8 +1306,8 @@ hipError_t launch_act_int8(const uint16_t *x, int64_t m, int64_t k, int8_t *code
 }
 
 // In one launch where one workgroup buckets and a row stays in a wave's
-// registers (6.7 us for 16 tokens x 2688, 10.3 for 1024; in two launches 4.4 +
-// 6.9 and 6.5 + 10.5), in two or four otherwise.
+// registers (6.2 to 8.0 us for 16 tokens x 2688, 10.2 to 13.8 for 1024; in two
+// launches 4.4 + 6.9 and 6.5 + 10.5), in two or four otherwise.
 hipError_t launch_moe_int8_prepare(const uint16_t *x, int64_t t, int64_t k, const int32_t *ids,
                                    int32_t topk, int32_t n_experts, int32_t *counts,
                                    int32_t *offsets, int32_t *perm, int32_t *inv, MoETile *tiles,
