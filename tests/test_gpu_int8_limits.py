@@ -132,3 +132,127 @@ def test_moe_weights_past_32_bits(dev, t, k, some):
     assert (np.abs(ref) > 0).mean() > 0.9
     err = np.abs(out[some].cpu().numpy().astype(np.float64) - ref)
     assert (err <= (topk + 5) * 2.0 ** -24 * mag).all()
+
+
+def _same_in_parts(y, xq, sx, wq, sw, part=1 << 20):
+    for i in range(0, y.shape[0], part):
+        at = slice(i, i + part)
+        if not torch.equal(y[at], _steps(xq[at], sx[at], wq, sw)):
+            return False
+    return True
+
+
+# rows and columns at their limit of 2^24, by every kernel family
+@pytest.mark.parametrize("m,k,n", [(2 ** 24, 32, 3), (2 ** 24, 96, 17), (1, 32, 2 ** 24),
+                                   (5, 64, 2 ** 24), (40, 32, 2 ** 24)])
+def test_linear_of_most_rows_and_columns(dev, m, k, n):
+    kp = _ops().int8_padded_k(k)
+    cache, wq, sw = _random_cache(dev, n, kp, 0.02, seed=n)
+    wq[:, k:] = 0
+    gen = torch.Generator(device=dev).manual_seed(m)
+    x = torch.randn(m, k, generator=gen, device=dev).to(torch.bfloat16)
+    some = sorted({0, m // 2, m - 1})
+    xq, sx = _ops().act_int8(x)
+    rq, rs = O.act_int8(x[some].view(torch.int16).cpu().numpy().view(np.uint16))
+    assert np.array_equal(xq[some, :k].cpu().numpy(), rq) and np.array_equal(sx[some].cpu(), rs)
+    y = _ops().linear_int8(x, cache, n)
+    if m > n:
+        assert _same_in_parts(y, xq, sx, wq, sw)
+    else:                                   # the transposed product's rows, the same steps
+        for i in range(0, n, 1 << 20):
+            at = slice(i, i + (1 << 20))
+            assert torch.equal(y[:, at], _steps(xq, sx, wq[at], sw[at]))
+
+
+def _moe_some(x, ids, g, some, caches, e, n1, k):
+    """The oracle's layer for some tokens, from the caches' codes and scales."""
+    used = set(ids[some].ravel().tolist())
+    lists = []
+    for (q, s), rows, cols in zip(caches, (n1, k), (k, n1)):
+        lists.append([(q[i * rows:(i + 1) * rows, :cols].cpu().numpy(),
+                       s[i * rows:(i + 1) * rows].cpu().numpy()) if i in used else None
+                      for i in range(e)])
+    bits = x[some].view(torch.int16).cpu().numpy().view(np.uint16)
+    return O.moe_int8(bits, ids[some], g[some], *lists)
+
+
+# the longest rows of both products, every expert in every slot, and the most pairs
+@pytest.mark.parametrize("t,e,topk,n1,k", [(1, 2, 1, 64, 131072), (9, 2, 2, 64, 131072),
+                                           (300, 2, 2, 64, 131072), (1, 2, 1, 131072, 64),
+                                           (9, 2, 2, 131072, 64), (300, 2, 2, 131072, 64),
+                                           (1, 512, 512, 32, 64), (7, 512, 300, 32, 64),
+                                           (500, 512, 512, 32, 64), (16774911, 8, 1, 32, 32)])
+def test_moe_of_the_longest_rows_and_the_most_pairs(dev, t, e, topk, n1, k):
+    kp, n1p = _ops().int8_padded_k(k), _ops().int8_padded_k(n1)
+    gain = 0.5 / max(k, n1) ** 0.5
+    c1, q1, s1 = _random_cache(dev, e * n1, kp, gain, seed=7)
+    c2, q2, s2 = _random_cache(dev, e * k, n1p, gain, seed=8)
+    q1[:, k:] = 0
+    q2[:, n1:] = 0
+    rng = np.random.default_rng(t + topk)
+    if t > 1000:
+        ids = rng.integers(0, e, (t, topk)).astype(np.int32)
+    else:
+        ids = np.stack([rng.permutation(e)[:topk] for _ in range(t)]).astype(np.int32)
+    g = rng.random((t, topk), np.float32)
+    gen = torch.Generator(device=dev).manual_seed(t)
+    x = torch.randn(t, k, generator=gen, device=dev).to(torch.bfloat16)
+    out = _ops().moe_grouped_int8(x, torch.from_numpy(ids).to(dev), torch.from_numpy(g).to(dev),
+                                  c1, c2, e, n1)
+    some = sorted({0, t // 3, t - 1})
+    ref, mag = _moe_some(x, ids, g, some, ((q1, s1), (q2, s2)), e, n1, k)
+    assert (np.abs(ref) > 0).mean() > 0.9
+    err = np.abs(out[some].cpu().numpy().astype(np.float64) - ref)
+    assert (err <= (topk + 5) * 2.0 ** -24 * mag).all()
+
+
+def _guarded(dev, shape, dtype, fill=7):
+    """A tensor inside a longer one of a known value, and a check of its margins."""
+    count, pad = int(np.prod(shape)), 256
+    held = torch.full((count + 2 * pad,), fill, dtype=dtype, device=dev)
+    return held[pad:pad + count].view(shape), lambda: bool(
+        (held[:pad] == fill).all() and (held[pad + count:] == fill).all())
+
+
+def test_memory_of_the_caller(dev):
+    """Caches, codes, outputs and scratch that the caller brings: the same results, and
+    nothing written outside."""
+    o = _ops()
+    m, k, n, e, topk, n1 = 37, 224, 96, 4, 2, 160
+    gen = torch.Generator(device=dev).manual_seed(9)
+    w = torch.randn(n, k, generator=gen, device=dev).to(torch.bfloat16)
+    x = torch.randn(m, k, generator=gen, device=dev).to(torch.bfloat16)
+    checks = []
+
+    def own(shape, dtype):
+        view, check = _guarded(dev, shape, dtype)
+        checks.append(check)
+        return view
+
+    cache = o.int8_cache_bf16(w)
+    assert torch.equal(o.int8_cache_bf16(w, own((o.int8_cache_size(n, k),), torch.uint8)), cache)
+    packed = o.pack(w.float(), I.sign_bits())
+    assert torch.equal(o.int8_cache(packed, I.sign_bits(),
+                                    own((o.int8_cache_size(n, k),), torch.uint8)),
+                       o.int8_cache(packed, I.sign_bits()))
+    size = o.linear_int8_workspace_size(m, k, n)
+    y = o.linear_int8(x, cache, n)
+    assert torch.equal(o.linear_int8(x, cache, n, own((m, n), torch.float32),
+                                     own((size,), torch.uint8)), y)
+    assert torch.equal(o.linear_int8_quantized(*o.act_int8(x), k, cache, n,
+                                               own((m, n), torch.float32)), y)
+    w1, w2 = (torch.randn(e * a, b, generator=gen, device=dev).to(torch.bfloat16)
+              for a, b in ((n1, k), (k, n1)))
+    c1, c2 = o.int8_cache_bf16(w1), o.int8_cache_bf16(w2)
+    lg = torch.randn(m, e, generator=gen, device=dev)
+    ids, g = o.moe_router_scored(lg, topk, renormalize=True)
+    own_ids, own_g = own((m, topk), torch.int32), own((m, topk), torch.float32)
+    o.moe_router_scored(lg, topk, renormalize=True, ids=own_ids, gates=own_g)
+    assert torch.equal(own_ids, ids) and torch.equal(own_g, g)
+    for t in (2, m):
+        size = o.moe_grouped_int8_workspace_size(t, topk, e, n1, k)
+        args = (x[:t], ids[:t], g[:t], c1, c2, e, n1)
+        assert torch.equal(o.moe_grouped_int8(*args, own((t, k), torch.float32),
+                                              own((size,), torch.uint8)),
+                           o.moe_grouped_int8(*args))
+    assert all(check() for check in checks)
