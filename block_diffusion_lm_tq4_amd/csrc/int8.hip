@@ -572,10 +572,10 @@ __global__ __launch_bounds__(64 * KW) void i8_skinny_kernel(I8Args g) {
 // is that of the register stream above, the row's codes broadcast to all
 // sixteen rows of the operand.
 //
-// m = 1, 2688 x 8192: 7.4 us against 8.6 for quantizer and product one after
-// the other, and one launch for the host instead of two (8.0 against 12.7 us
-// a call); 8192 x 2688 7.7 against 10.8.  From two rows on the wave's own quantization costs more than it
-// saves (10.2 against 9.1 us).
+// m = 1, 2688 x 8192: 7.4 us against 8.6 for quantizer and product one after the
+// other, and one launch for the host instead of two (8.0 against 12.7 us a call);
+// 8192 x 2688 7.7 against 10.8.  From two rows on the wave's own quantization costs
+// more than it saves (10.2 against 9.1 us).
 
 constexpr int kDirectSteps = 16;  // steps of 64 k per wave
 

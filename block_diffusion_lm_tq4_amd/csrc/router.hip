@@ -271,8 +271,8 @@ __global__ __launch_bounds__(256) void router_f64_kernel(
   const int wave = threadIdx.x / 64;
   const int64_t tok = static_cast<int64_t>(blockIdx.x) * 4 + wave;
   if (tok >= t) return;
-  route_token_f64<kPer, kPer>(logits + tok * cfg.n_experts, cfg, bias, group[wave], threadIdx.x % 64,
-                  ids + tok * cfg.topk, w + tok * cfg.topk);
+  route_token_f64<kPer, kPer>(logits + tok * cfg.n_experts, cfg, bias, group[wave],
+                              threadIdx.x % 64, ids + tok * cfg.topk, w + tok * cfg.topk);
 }
 
 // ---- four tokens by one wave, decided in fp32 where that decides --------------
