@@ -85,6 +85,26 @@ SIGNATURES = {
                                             _P, _P, _SZ, _P]),
     "tq4_moe_router_scored": (ctypes.c_int, [_P, _I64, _I32, _I32, ctypes.c_int, _P, _I32, _I32,
                                              ctypes.c_int, ctypes.c_float, _P, _P, _P]),
+    "tq4_mxfp4_cache_size": (_SZ, [_I64, _I64]),
+    "tq4_mxfp4_cache": (ctypes.c_int, [_P, _I64, _I64, _U32, _P, _P]),
+    "tq4_mxfp4_cache_bf16": (ctypes.c_int, [_P, _I64, _I64, _P, _P]),
+    "tq4_act_mxfp4": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P]),
+    "tq4_mxfp4_values": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P]),
+    "tq4_linear_mxfp4_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "tq4_linear_mxfp4": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _P, _P, _SZ, _P]),
+    "tq4_linear_mxfp4_epilogue": (ctypes.c_int,
+                                  [_P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "tq4_linear_mxfp4_epilogue_bf16": (ctypes.c_int,
+                                       [_P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "tq4_linear_mxfp4_quantized": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I64, _P, _P]),
+    "tq4_moe_grouped_mxfp4_workspace_size": (_SZ, [_I64, _I32, _I32, _I64, _I64]),
+    "tq4_moe_grouped_mxfp4": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I32, _I32, _P, _I64, _P,
+                                             _P, _P, _SZ, _P]),
+    "tq4_moe_balance_workspace_size": (_SZ, [_I64, _I32]),
+    "tq4_moe_balance": (ctypes.c_int, [_P, _I64, _I32, _P, _I32, ctypes.c_int, _P, _P, _P, _P, _P,
+                                       _SZ, _P]),
+    "tq4_moe_router_backward": (ctypes.c_int, [_P, _I64, _I32, _P, _I32, ctypes.c_int, _P,
+                                               ctypes.c_int, ctypes.c_float, _P, _P, _P, _P, _P]),
     "tq4_moe_router": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P]),
     "tq4_read_probe": (ctypes.c_int, [_P, _I64, _P, _P]),
 }

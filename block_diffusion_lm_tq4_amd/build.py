@@ -35,6 +35,8 @@ SOURCES = {
     "fp8.hip": ["-ffp-contract=off"],
     "int8.hip": ["-ffp-contract=off"],
     "router.hip": ["-ffp-contract=off"],
+    "mxfp4.hip": ["-ffp-contract=off"],
+    "balance.hip": ["-ffp-contract=off"],
 }
 
 ARCH = "gfx950"

@@ -8,7 +8,7 @@
 
 #include "../../include/tq4.h"
 #include "moe_block.h"
-#include "int8_router.h"
+#include "mxfp4.h"
 
 namespace {
 
@@ -944,6 +944,320 @@ int tq4_moe_router_scored(const float *logits, int64_t t, int32_t n_experts, int
   cfg.scale = scale;
   return device_status(
       tq4::launch_router_scored(logits, t, cfg, bias, topk_ids, topk_w, as_stream(stream)));
+}
+
+// ---- MXFP4 products --------------------------------------------------------
+
+namespace {
+
+constexpr int64_t kFp4MaxK = int64_t{1} << 20;
+
+bool fp4_sizes_ok(int64_t rows, int64_t k) {
+  return rows >= 0 && rows <= INT32_MAX && k >= 0 && k % 32 == 0 && k <= kFp4MaxK;
+}
+
+bool fp4_linear_sizes_ok(int64_t m, int64_t k, int64_t n) {
+  return fp4_sizes_ok(m, k) && fp4_sizes_ok(n, k) && m <= kI8MaxLinearRows &&
+         n <= kI8MaxLinearRows;
+}
+
+size_t fp4_codes_bytes(int64_t rows, int64_t k) {
+  return static_cast<size_t>(rows) * static_cast<size_t>(tq4::mxfp4_padded_k(k) / 2);
+}
+
+size_t fp4_scales_bytes(int64_t rows, int64_t k) {
+  return static_cast<size_t>(rows) * static_cast<size_t>(tq4::mxfp4_padded_k(k) / 32);
+}
+
+int linear_fp4_impl(const uint16_t *x_bf16, const uint8_t *x_codes, const uint8_t *x_scales,
+                    int64_t m, int64_t k, const uint8_t *cache, int64_t n, const tq4::Tail &tail,
+                    void *y, void *workspace, size_t workspace_bytes, void *stream) {
+  if (!fp4_linear_sizes_ok(m, k, n)) return TQ4_E_SHAPE;
+  if (m == 0 || n == 0) return TQ4_OK;
+  const int st = linear_tail_args(m, n, tail, y);
+  if (st != TQ4_OK) return st;
+  hipStream_t s = as_stream(stream);
+  float *yf = static_cast<float *>(y);
+  const bool plain = tail.bias == nullptr && tail.residual == nullptr && !tail.bf16;
+  if (k == 0)
+    return device_status(plain ? tq4::launch_fill_zero(yf, m * n, s)
+                               : tq4::launch_tail_only(tail, m, n, yf, s));
+  if (cache == nullptr) return TQ4_E_NULL;
+  if (!aligned(cache, 16)) return TQ4_E_ALIGN;
+  const uint8_t *w_scales = cache + fp4_codes_bytes(n, k);
+  const uint64_t y_bytes = static_cast<uint64_t>(m) * n * (tail.bf16 ? 2 : 4);
+  if (x_bf16 != nullptr) {
+    if (!aligned(x_bf16, 16)) return TQ4_E_ALIGN;
+    const bool direct = tq4::mxfp4_direct_fits(m);
+    if (!direct) {
+      const int ws = check_workspace(workspace, workspace_bytes,
+                                     tq4_linear_mxfp4_workspace_size(m, k, n));
+      if (ws != TQ4_OK) return ws;
+    }
+    // few rows are read by workgroups while others store
+    if (overlap(x_bf16, static_cast<uint64_t>(m) * k * 2, y, y_bytes)) return TQ4_E_SHAPE;
+    if (direct)
+      return device_status(
+          tq4::launch_linear_mxfp4_direct(x_bf16, m, k, cache, w_scales, n, tail, y, s));
+    uint8_t *xq = static_cast<uint8_t *>(workspace);
+    uint8_t *xs = xq + align_up(fp4_codes_bytes(m, k));
+    const hipError_t e = tq4::launch_act_mxfp4(x_bf16, m, k, xq, xs, s);
+    if (e != hipSuccess) return TQ4_E_DEVICE;
+    x_codes = xq;
+    x_scales = xs;
+  } else {
+    if (x_codes == nullptr || x_scales == nullptr) return TQ4_E_NULL;
+    if (!aligned(x_codes, 16) || !aligned(x_scales, 4)) return TQ4_E_ALIGN;
+    if (overlap(x_codes, fp4_codes_bytes(m, k), y, y_bytes) ||
+        overlap(x_scales, fp4_scales_bytes(m, k), y, y_bytes))
+      return TQ4_E_SHAPE;
+  }
+  return device_status(
+      tq4::launch_linear_mxfp4(x_codes, x_scales, m, k, cache, w_scales, n, tail, y, s));
+}
+
+// A call that is given bf16 rows needs them wherever it reads them.
+int linear_fp4_bf16(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache, int64_t n,
+                    const tq4::Tail &tail, void *y, void *workspace, size_t workspace_bytes,
+                    void *stream) {
+  if (x_bf16 == nullptr && m > 0 && n > 0 && k > 0 && fp4_linear_sizes_ok(m, k, n))
+    return TQ4_E_NULL;
+  return linear_fp4_impl(x_bf16, nullptr, nullptr, m, k, cache, n, tail, y, workspace,
+                         workspace_bytes, stream);
+}
+
+}  // namespace
+
+size_t tq4_mxfp4_cache_size(int64_t n, int64_t k) {
+  if (!fp4_sizes_ok(n, k) || k == 0) return 0;
+  return fp4_codes_bytes(n, k) + fp4_scales_bytes(n, k);
+}
+
+int tq4_mxfp4_cache(const uint8_t *packed, int64_t n, int64_t k, uint32_t sign_bits,
+                    uint8_t *cache, void *stream) {
+  if (!fp4_sizes_ok(n, k)) return TQ4_E_SHAPE;
+  if (n == 0 || k == 0) return TQ4_OK;
+  if (packed == nullptr || cache == nullptr) return TQ4_E_NULL;
+  if (!aligned(packed, 4) || !aligned(cache, 16)) return TQ4_E_ALIGN;
+  return device_status(tq4::launch_mxfp4_cache(packed, n, k, sign_bits, cache,
+                                               cache + fp4_codes_bytes(n, k), as_stream(stream)));
+}
+
+int tq4_mxfp4_cache_bf16(const uint16_t *w_bf16, int64_t n, int64_t k, uint8_t *cache,
+                         void *stream) {
+  if (!fp4_sizes_ok(n, k)) return TQ4_E_SHAPE;
+  if (n == 0 || k == 0) return TQ4_OK;
+  if (w_bf16 == nullptr || cache == nullptr) return TQ4_E_NULL;
+  if (!aligned(w_bf16, 16) || !aligned(cache, 16)) return TQ4_E_ALIGN;
+  return device_status(tq4::launch_act_mxfp4(w_bf16, n, k, cache, cache + fp4_codes_bytes(n, k),
+                                             as_stream(stream)));
+}
+
+int tq4_act_mxfp4(const uint16_t *x_bf16, int64_t m, int64_t k, uint8_t *codes, uint8_t *scales,
+                  void *stream) {
+  if (!fp4_sizes_ok(m, k)) return TQ4_E_SHAPE;
+  if (m == 0 || k == 0) return TQ4_OK;
+  if (x_bf16 == nullptr || codes == nullptr || scales == nullptr) return TQ4_E_NULL;
+  if (!aligned(x_bf16, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return TQ4_E_ALIGN;
+  return device_status(tq4::launch_act_mxfp4(x_bf16, m, k, codes, scales, as_stream(stream)));
+}
+
+int tq4_mxfp4_values(const uint8_t *codes, const uint8_t *scales, int64_t m, int64_t k,
+                     uint16_t *values_bf16, void *stream) {
+  if (!fp4_sizes_ok(m, k)) return TQ4_E_SHAPE;
+  if (m == 0 || k == 0) return TQ4_OK;
+  if (codes == nullptr || scales == nullptr || values_bf16 == nullptr) return TQ4_E_NULL;
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(values_bf16, 16))
+    return TQ4_E_ALIGN;
+  return device_status(
+      tq4::launch_mxfp4_values(codes, scales, m, k, values_bf16, as_stream(stream)));
+}
+
+size_t tq4_linear_mxfp4_workspace_size(int64_t m, int64_t k, int64_t n) {
+  if (!fp4_linear_sizes_ok(m, k, n)) return 0;
+  if (m == 0 || n == 0 || k == 0 || tq4::mxfp4_direct_fits(m)) return 0;
+  return align_up(fp4_codes_bytes(m, k)) + align_up(fp4_scales_bytes(m, k));
+}
+
+int tq4_linear_mxfp4(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache, int64_t n,
+                     float *y, void *workspace, size_t workspace_bytes, void *stream) {
+  return linear_fp4_bf16(x_bf16, m, k, cache, n, tq4::Tail{}, y, workspace, workspace_bytes,
+                         stream);
+}
+
+int tq4_linear_mxfp4_epilogue(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache,
+                              int64_t n, const float *bias, const float *residual, float *y,
+                              void *workspace, size_t workspace_bytes, void *stream) {
+  return linear_fp4_bf16(x_bf16, m, k, cache, n, tq4::Tail{bias, residual, 0}, y, workspace,
+                         workspace_bytes, stream);
+}
+
+int tq4_linear_mxfp4_epilogue_bf16(const uint16_t *x_bf16, int64_t m, int64_t k,
+                                   const uint8_t *cache, int64_t n, const float *bias,
+                                   const uint16_t *residual_bf16, uint16_t *y_bf16,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+  return linear_fp4_bf16(x_bf16, m, k, cache, n, tq4::Tail{bias, residual_bf16, 1}, y_bf16,
+                         workspace, workspace_bytes, stream);
+}
+
+int tq4_linear_mxfp4_quantized(const uint8_t *x_codes, const uint8_t *x_scales, int64_t m,
+                               int64_t k, const uint8_t *cache, int64_t n, float *y,
+                               void *stream) {
+  return linear_fp4_impl(nullptr, x_codes, x_scales, m, k, cache, n, tq4::Tail{}, y, nullptr, 0,
+                         stream);
+}
+
+namespace {
+
+struct MoEFp4Layout {
+  int tile_rows;
+  int64_t max_tiles;
+  size_t counts, offsets, perm, inv, tiles, meta, xq, xs, hq, hs, o, total;
+};
+
+MoEFp4Layout moe_fp4_layout(int64_t t, int32_t topk, int32_t e, int64_t n1, int64_t k) {
+  const int64_t pairs = t * topk;
+  MoEFp4Layout l{};
+  l.tile_rows = tq4::mxfp4_moe_tile_rows(pairs, e);
+  const int64_t busy = pairs < e ? pairs : e;
+  l.max_tiles = pairs / l.tile_rows + busy + 1;
+  const size_t p = static_cast<size_t>(pairs);
+  size_t off = 0;
+  l.counts = off;  off += align_up(sizeof(int32_t) * e);
+  l.offsets = off; off += align_up(sizeof(int32_t) * (e + 1));
+  l.perm = off;    off += align_up(sizeof(int32_t) * p);
+  l.inv = off;     off += align_up(sizeof(int32_t) * p);
+  l.tiles = off;   off += align_up(sizeof(MoETile) * static_cast<size_t>(l.max_tiles));
+  l.meta = off;    off += kAlign;
+  l.xq = off;      off += align_up(fp4_codes_bytes(t, k));
+  l.xs = off;      off += align_up(fp4_scales_bytes(t, k));
+  l.hq = off;      off += align_up(fp4_codes_bytes(pairs, n1));
+  l.hs = off;      off += align_up(fp4_scales_bytes(pairs, n1));
+  l.o = off;       off += align_up(p * static_cast<size_t>(k) * 4);
+  l.total = off;
+  return l;
+}
+
+bool moe_fp4_shape_ok(int64_t t, int32_t topk, int32_t e, int64_t n1, int64_t k) {
+  if (t < 0 || t > INT32_MAX || topk < 1 || e < 1 || e > 512 || topk > e) return false;
+  if (n1 <= 0 || k <= 0 || !fp4_sizes_ok(1, n1) || !fp4_sizes_ok(1, k)) return false;
+  // 32-bit offsets into the code arrays
+  if (t * (tq4::mxfp4_padded_k(k) / 2) > INT32_MAX || t * topk > INT32_MAX ||
+      t * topk * (tq4::mxfp4_padded_k(n1) / 2) > INT32_MAX)
+    return false;
+  return moe_fp4_layout(t, topk, e, n1, k).max_tiles <= 65535;
+}
+
+}  // namespace
+
+size_t tq4_moe_grouped_mxfp4_workspace_size(int64_t t, int32_t topk, int32_t n_experts, int64_t n1,
+                                            int64_t k) {
+  if (!moe_fp4_shape_ok(t, topk, n_experts, n1, k)) return 0;
+  return moe_fp4_layout(t, topk, n_experts, n1, k).total;
+}
+
+int tq4_moe_grouped_mxfp4(const uint16_t *x_bf16, int64_t t, int64_t k, const int32_t *topk_ids,
+                          const float *topk_w, int32_t topk, int32_t n_experts,
+                          const uint8_t *w1_cache, int64_t n1, const uint8_t *w2_cache, float *out,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+  if (!moe_fp4_shape_ok(t, topk, n_experts, n1, k)) return TQ4_E_SHAPE;
+  if (t == 0) return TQ4_OK;
+  if (x_bf16 == nullptr || topk_ids == nullptr || topk_w == nullptr || w1_cache == nullptr ||
+      w2_cache == nullptr || out == nullptr)
+    return TQ4_E_NULL;
+  if (!aligned(x_bf16, 16) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+      !aligned(w1_cache, 16) || !aligned(w2_cache, 16) || !aligned(out, 16))
+    return TQ4_E_ALIGN;
+  const MoEFp4Layout l = moe_fp4_layout(t, topk, n_experts, n1, k);
+  if (workspace == nullptr || workspace_bytes < l.total) return TQ4_E_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return TQ4_E_ALIGN;
+  char *ws = static_cast<char *>(workspace);
+  int32_t *counts = reinterpret_cast<int32_t *>(ws + l.counts);
+  int32_t *offsets = reinterpret_cast<int32_t *>(ws + l.offsets);
+  int32_t *perm = reinterpret_cast<int32_t *>(ws + l.perm);
+  int32_t *inv = reinterpret_cast<int32_t *>(ws + l.inv);
+  MoETile *tiles = reinterpret_cast<MoETile *>(ws + l.tiles);
+  int32_t *meta = reinterpret_cast<int32_t *>(ws + l.meta);
+  uint8_t *xq = reinterpret_cast<uint8_t *>(ws + l.xq);
+  uint8_t *xs = reinterpret_cast<uint8_t *>(ws + l.xs);
+  uint8_t *hq = reinterpret_cast<uint8_t *>(ws + l.hq);
+  uint8_t *hs = reinterpret_cast<uint8_t *>(ws + l.hs);
+  float *o = reinterpret_cast<float *>(ws + l.o);
+  const int64_t pairs = t * topk;
+  const uint8_t *w1_scales = w1_cache + fp4_codes_bytes(n_experts * n1, k);
+  const uint8_t *w2_scales = w2_cache + fp4_codes_bytes(n_experts * k, n1);
+  hipStream_t s = as_stream(stream);
+  hipError_t e = tq4::launch_act_mxfp4(x_bf16, t, k, xq, xs, s);
+  if (e == hipSuccess)
+    e = tq4::launch_route(topk_ids, pairs, topk, n_experts, counts, offsets, perm, inv, tiles,
+                          meta, l.tile_rows, nullptr, s);
+  if (e == hipSuccess)
+    e = tq4::launch_moe_mxfp4(0, l.tile_rows, xq, xs, t, k, perm, topk, w1_cache, w1_scales, n1,
+                              tiles, meta, l.max_tiles, nullptr, hq, hs, s);
+  if (e == hipSuccess)
+    e = tq4::launch_moe_mxfp4(1, l.tile_rows, hq, hs, pairs, n1, perm, topk, w2_cache, w2_scales,
+                              k, tiles, meta, l.max_tiles, o, nullptr, nullptr, s);
+  if (e == hipSuccess) e = tq4::launch_combine(o, inv, topk_w, t, topk, k, out, s);
+  return device_status(e);
+}
+
+// ---- the router's training step ---------------------------------------------
+
+namespace {
+
+bool balance_sizes_ok(int64_t t, int32_t n_experts, int32_t topk, int score) {
+  // pairs are counted in int32
+  return t >= 0 && n_experts >= 1 && n_experts <= 512 && topk >= 1 && topk <= n_experts &&
+         t <= INT32_MAX / topk && (score == TQ4_SCORE_SOFTMAX || score == TQ4_SCORE_SIGMOID);
+}
+
+}  // namespace
+
+size_t tq4_moe_balance_workspace_size(int64_t t, int32_t n_experts) {
+  if (t < 0 || t > INT32_MAX || n_experts < 1 || n_experts > 512) return 0;
+  return align_up(static_cast<size_t>(tq4::balance_groups(t)) * (2 * n_experts + 1) * 4);
+}
+
+int tq4_moe_balance(const float *logits, int64_t t, int32_t n_experts, const int32_t *topk_ids,
+                    int32_t topk, int score, float *loss, int32_t *counts, int32_t *tokens,
+                    float *mean_p, void *workspace, size_t workspace_bytes, void *stream) {
+  if (!balance_sizes_ok(t, n_experts, topk, score)) return TQ4_E_SHAPE;
+  if (loss == nullptr || counts == nullptr || tokens == nullptr || mean_p == nullptr)
+    return TQ4_E_NULL;
+  if (t > 0 && (logits == nullptr || topk_ids == nullptr)) return TQ4_E_NULL;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) ||
+      !aligned(tokens, 4) || !aligned(mean_p, 4))
+    return TQ4_E_ALIGN;
+  const int st = check_workspace(workspace, workspace_bytes,
+                                 tq4_moe_balance_workspace_size(t, n_experts));
+  if (st != TQ4_OK) return st;
+  const tq4::BalanceArgs a{logits, topk_ids, t, n_experts, topk, score == TQ4_SCORE_SIGMOID};
+  return device_status(
+      tq4::launch_moe_balance(a, loss, counts, tokens, mean_p, workspace, as_stream(stream)));
+}
+
+int tq4_moe_router_backward(const float *logits, int64_t t, int32_t n_experts,
+                            const int32_t *topk_ids, int32_t topk, int score, const float *dgates,
+                            int renormalize, float scale, const int32_t *counts,
+                            const int32_t *tokens, const float *dloss, float *dlogits,
+                            void *stream) {
+  if (!balance_sizes_ok(t, n_experts, topk, score)) return TQ4_E_SHAPE;
+  if (t == 0) return TQ4_OK;
+  if (logits == nullptr || topk_ids == nullptr || dlogits == nullptr) return TQ4_E_NULL;
+  // the loss's three arguments come together
+  const bool loss = counts != nullptr;
+  if ((tokens != nullptr) != loss || (dloss != nullptr) != loss) return TQ4_E_NULL;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(dgates, 4) || !aligned(counts, 4) ||
+      !aligned(tokens, 4) || !aligned(dloss, 4) || !aligned(dlogits, 4))
+    return TQ4_E_ALIGN;
+  const uint64_t pairs = static_cast<uint64_t>(t) * topk;
+  const uint64_t bytes = static_cast<uint64_t>(t) * n_experts * 4;
+  if (overlap(dlogits, bytes, logits, bytes) || overlap(dlogits, bytes, topk_ids, pairs * 4) ||
+      (dgates != nullptr && overlap(dlogits, bytes, dgates, pairs * 4)))
+    return TQ4_E_SHAPE;
+  const tq4::RouterGradArgs a{{logits, topk_ids, t, n_experts, topk, score == TQ4_SCORE_SIGMOID},
+                              dgates, renormalize, scale, counts, tokens, dloss, dlogits};
+  return device_status(tq4::launch_router_backward(a, as_stream(stream)));
 }
 
 int tq4_read_probe(const void *src, int64_t bytes, float *sink, void *stream) {

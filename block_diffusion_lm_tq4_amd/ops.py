@@ -764,6 +764,291 @@ def moe_router_scored(logits: torch.Tensor, topk: int, score: str = "softmax",
     return ids, gates
 
 
+# ---------------------------------------------------------------------------
+# MXFP4 products and the router's training step.  Scratch as for the int8 products.
+
+def mxfp4_padded_k(k: int) -> int:
+    return (k + 127) // 128 * 128
+
+
+def mxfp4_cache_size(n: int, k: int) -> int:
+    return int(lib().tq4_mxfp4_cache_size(n, k))
+
+
+def _mxfp4_bytes(n: int, k: int) -> int:
+    """tq4_mxfp4_cache_size of valid sizes."""
+    kp = mxfp4_padded_k(k)
+    return n * (kp // 2) + n * (kp // 32)
+
+
+def _mxfp4_cache_out(out, n, k, dev):
+    size = mxfp4_cache_size(n, k)
+    if out is None:
+        return torch.empty(size, dtype=torch.uint8, device=dev)
+    _arg_on(out, "out", torch.uint8, dev)
+    _require(out.numel() >= size, "out is smaller than tq4_mxfp4_cache_size(n, k)")
+    return out
+
+
+def mxfp4_cache(packed: torch.Tensor, sign_bits: int,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """packed [n, k/32, 20] -> the MXFP4 weight cache (flat uint8: codes [n][kp/2],
+    then scale bytes [n][kp/32]) (tq4_mxfp4_cache)."""
+    _cuda_contig(packed, "packed", torch.uint8)
+    _require(packed.dim() == 3 and packed.shape[2] == BLOCK_BYTES, "packed must be [n, k/32, 20]")
+    n, k = packed.shape[0], packed.shape[1] * BLOCK
+    out = _mxfp4_cache_out(out, n, k, packed.device)
+    _call("tq4_mxfp4_cache", packed.device, packed.data_ptr(), n, k, sign_bits & 0xFFFFFFFF,
+          out.data_ptr())
+    return out
+
+
+def mxfp4_cache_bf16(w: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """bf16 weights [n, k] -> the MXFP4 weight cache (tq4_mxfp4_cache_bf16)."""
+    _cuda_contig(w, "w", torch.bfloat16)
+    _require(w.dim() == 2, "w must be [n, k]")
+    n, k = w.shape
+    out = _mxfp4_cache_out(out, n, k, w.device)
+    _call("tq4_mxfp4_cache_bf16", w.device, w.data_ptr(), n, k, out.data_ptr())
+    return out
+
+
+def mxfp4_cache_experts(packed: torch.Tensor, sign_bits: int) -> torch.Tensor:
+    """Experts' packed weights [E, n, k/32, 20] -> the MXFP4 cache of the stacked
+    [E * n, k] matrix (the layout tq4_moe_grouped_mxfp4 takes)."""
+    _require(packed.dim() == 4, "packed must be [E, n, k/32, 20]")
+    e, n, kb, bb = packed.shape
+    return mxfp4_cache(packed.view(e * n, kb, bb), sign_bits)
+
+
+def mxfp4_cache_views(cache: torch.Tensor, n: int, k: int) -> tuple[torch.Tensor, torch.Tensor]:
+    """(codes [n, kp/2], scales [n, kp/32]) views of a flat cache."""
+    kp = mxfp4_padded_k(k)
+    split = n * kp // 2
+    return cache[:split].view(n, kp // 2), cache[split:split + n * kp // 32].view(n, kp // 32)
+
+
+def act_mxfp4(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """bf16 x [m, k] -> (codes [m, kp/2], scales [m, kp/32]) uint8 (tq4_act_mxfp4)."""
+    _cuda_contig(x, "x", torch.bfloat16)
+    _require(x.dim() == 2, "x must be [m, k]")
+    m, k = x.shape
+    kp = mxfp4_padded_k(k)
+    codes = torch.empty((m, kp // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((m, kp // 32), dtype=torch.uint8, device=x.device)
+    _call("tq4_act_mxfp4", x.device, x.data_ptr(), m, k, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def mxfp4_values(codes: torch.Tensor, scales: torch.Tensor, k: int,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of codes [m, kp/2] and scale bytes [m, kp/32], bf16 [m, k]
+    (tq4_mxfp4_values)."""
+    _cuda_contig(codes, "codes", torch.uint8)
+    dev = codes.device
+    _arg_on(scales, "scales", torch.uint8, dev)
+    kp = mxfp4_padded_k(k)
+    _require(codes.dim() == 2 and codes.shape[1] == kp // 2, "codes must be [m, kp/2]")
+    m = codes.shape[0]
+    _require(tuple(scales.shape) == (m, kp // 32), "scales must be [m, kp/32]")
+    if out is None:
+        out = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
+    else:
+        _arg_on(out, "out", torch.bfloat16, dev)
+        _require(tuple(out.shape) == (m, k), "out must be [m, k]")
+    _call("tq4_mxfp4_values", dev, codes.data_ptr(), scales.data_ptr(), m, k, out.data_ptr())
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def linear_mxfp4_workspace_size(m: int, k: int, n: int) -> int:
+    return int(lib().tq4_linear_mxfp4_workspace_size(m, k, n))
+
+
+def _linear_mxfp4(fn, x, cache, n, tail, out, workspace, ydtype):
+    _cuda_contig(x, "x", torch.bfloat16)
+    _require(x.dim() == 2, "x must be [m, k]")
+    m, k = x.shape
+    dev = x.device
+    _arg_on(cache, "cache", torch.uint8, dev)
+    _require(cache.numel() >= _mxfp4_bytes(n, k), "cache too small for [n, k]")
+    ptrs = []
+    if tail is not None:
+        bias, residual = tail
+        if bias is not None:
+            _arg_on(bias, "bias", torch.float32, dev)
+            _require(tuple(bias.shape) == (n,), "bias must be [n]")
+        if residual is not None:
+            _arg_on(residual, "residual", ydtype, dev)
+            _require(tuple(residual.shape) == (m, n), "residual must be [m, n]")
+        ptrs = [_ptr(bias), _ptr(residual)]
+    if out is None:
+        out = torch.empty((m, n), dtype=ydtype, device=dev)
+    else:
+        _arg_on(out, "out", ydtype, dev)
+        _require(tuple(out.shape) == (m, n), "out must be [m, n]")
+    held, ws, ws_size = _scratch(workspace, linear_mxfp4_workspace_size(m, k, n), dev)
+    _call(fn, dev, x.data_ptr(), m, k, cache.data_ptr(), n, *ptrs, out.data_ptr(), ws, ws_size)
+    return out
+
+
+def linear_mxfp4(x: torch.Tensor, cache: torch.Tensor, n: int, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y = x . W^T in MXFP4 from the cache of an [n, k] matrix, fp32 [m, n]
+    (tq4_linear_mxfp4).  `out` may not overlap x."""
+    return _linear_mxfp4("tq4_linear_mxfp4", x, cache, n, None, out, workspace, torch.float32)
+
+
+def linear_mxfp4_epilogue(x: torch.Tensor, cache: torch.Tensor, n: int,
+                          bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                          out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """linear_mxfp4 + bias + residual, fp32 [m, n] (tq4_linear_mxfp4_epilogue); the
+    residual may be `out` itself, which may not overlap x."""
+    return _linear_mxfp4("tq4_linear_mxfp4_epilogue", x, cache, n, (bias, residual), out,
+                         workspace, torch.float32)
+
+
+def linear_mxfp4_epilogue_bf16(x: torch.Tensor, cache: torch.Tensor, n: int,
+                               bias: torch.Tensor | None = None,
+                               residual: torch.Tensor | None = None,
+                               out: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """bf16(linear_mxfp4 + bias + residual), bf16 [m, n], the residual bf16
+    (tq4_linear_mxfp4_epilogue_bf16); it may be x, or `out`, which may not overlap
+    x."""
+    return _linear_mxfp4("tq4_linear_mxfp4_epilogue_bf16", x, cache, n, (bias, residual), out,
+                         workspace, torch.bfloat16)
+
+
+def linear_mxfp4_quantized(x_codes: torch.Tensor, x_scales: torch.Tensor, k: int,
+                           cache: torch.Tensor, n: int,
+                           out: torch.Tensor | None = None) -> torch.Tensor:
+    """y from activations already quantized by act_mxfp4 (tq4_linear_mxfp4_quantized)."""
+    _cuda_contig(x_codes, "x_codes", torch.uint8)
+    dev = x_codes.device
+    _arg_on(x_scales, "x_scales", torch.uint8, dev)
+    _arg_on(cache, "cache", torch.uint8, dev)
+    kp = mxfp4_padded_k(k)
+    _require(x_codes.dim() == 2 and x_codes.shape[1] == kp // 2, "x_codes must be [m, kp/2]")
+    m = x_codes.shape[0]
+    _require(tuple(x_scales.shape) == (m, kp // 32), "x_scales must be [m, kp/32]")
+    _require(cache.numel() >= _mxfp4_bytes(n, k), "cache too small for [n, k]")
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.float32, device=dev)
+    else:
+        _arg_on(out, "out", torch.float32, dev)
+        _require(tuple(out.shape) == (m, n), "out must be [m, n]")
+    _call("tq4_linear_mxfp4_quantized", dev, x_codes.data_ptr(), x_scales.data_ptr(), m, k,
+          cache.data_ptr(), n, out.data_ptr())
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def moe_grouped_mxfp4_workspace_size(t: int, topk: int, n_experts: int, n1: int, k: int) -> int:
+    return int(lib().tq4_moe_grouped_mxfp4_workspace_size(t, topk, n_experts, n1, k))
+
+
+def moe_grouped_mxfp4(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
+                      w1_cache: torch.Tensor, w2_cache: torch.Tensor, n_experts: int, n1: int,
+                      out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The MoE layer on MXFP4 expert caches (tq4_moe_grouped_mxfp4); fp32 [t, k]."""
+    _cuda_contig(x, "x", torch.bfloat16)
+    _require(x.dim() == 2, "x must be [t, k]")
+    t, k = x.shape
+    dev = x.device
+    _arg_on(topk_ids, "topk_ids", torch.int32, dev)
+    _arg_on(topk_w, "topk_w", torch.float32, dev)
+    _arg_on(w1_cache, "w1_cache", torch.uint8, dev)
+    _arg_on(w2_cache, "w2_cache", torch.uint8, dev)
+    _require(topk_ids.dim() == 2 and topk_ids.shape[0] == t, "topk_ids must be [t, topk]")
+    topk = topk_ids.shape[1]
+    _require(tuple(topk_w.shape) == (t, topk), "topk_w must be [t, topk]")
+    _require(w1_cache.numel() >= _mxfp4_bytes(n_experts * n1, k),
+             "w1_cache too small for [E * n1, k]")
+    _require(w2_cache.numel() >= _mxfp4_bytes(n_experts * k, n1),
+             "w2_cache too small for [E * k, n1]")
+    if out is None:
+        out = torch.empty((t, k), dtype=torch.float32, device=dev)
+    else:
+        _arg_on(out, "out", torch.float32, dev)
+        _require(tuple(out.shape) == (t, k), "out must be [t, k]")
+    held, ws, ws_size = _scratch(
+        workspace, moe_grouped_mxfp4_workspace_size(t, topk, n_experts, n1, k), dev)
+    _call("tq4_moe_grouped_mxfp4", dev, x.data_ptr(), t, k, topk_ids.data_ptr(),
+          topk_w.data_ptr(), topk, n_experts, w1_cache.data_ptr(), n1, w2_cache.data_ptr(),
+          out.data_ptr(), ws, ws_size)
+    return out
+
+
+def _router_args(logits, topk_ids, score):
+    _cuda_contig(logits, "logits", torch.float32)
+    _require(logits.dim() == 2, "logits must be [t, n_experts]")
+    _require(score in SCORES, "score must be 'softmax' or 'sigmoid'")
+    _arg_on(topk_ids, "topk_ids", torch.int32, logits.device)
+    _require(topk_ids.dim() == 2 and topk_ids.shape[0] == logits.shape[0],
+             "topk_ids must be [t, topk]")
+    return logits.shape[0], logits.shape[1], topk_ids.shape[1]
+
+
+@functools.lru_cache(maxsize=4096)
+def moe_balance_workspace_size(t: int, n_experts: int) -> int:
+    return int(lib().tq4_moe_balance_workspace_size(t, n_experts))
+
+
+def moe_balance(logits: torch.Tensor, topk_ids: torch.Tensor, score: str = "softmax",
+                workspace: torch.Tensor | None = None):
+    """Balance statistics of a router's choices (tq4_moe_balance): (loss fp32 scalar,
+    counts int32 [n_experts], tokens int32 scalar, mean_p fp32 [n_experts]).  The
+    gradient of the loss is moe_router_backward's."""
+    t, e, topk = _router_args(logits, topk_ids, score)
+    dev = logits.device
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    counts = torch.empty(e, dtype=torch.int32, device=dev)
+    tokens = torch.empty((), dtype=torch.int32, device=dev)
+    mean_p = torch.empty(e, dtype=torch.float32, device=dev)
+    held, ws, ws_size = _scratch(workspace, moe_balance_workspace_size(t, e), dev)
+    _call("tq4_moe_balance", dev, logits.data_ptr(), t, e, topk_ids.data_ptr(), topk,
+          SCORES[score], loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(),
+          mean_p.data_ptr(), ws, ws_size)
+    return loss, counts, tokens, mean_p
+
+
+def moe_router_backward(logits: torch.Tensor, topk_ids: torch.Tensor,
+                        dgates: torch.Tensor | None = None, score: str = "softmax",
+                        renormalize: bool = False, scale: float = 1.0,
+                        counts: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                        dloss: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of moe_router_scored's gates (dgates fp32 [t, topk]) and of
+    moe_balance's loss (dloss, one fp32 value, with its counts and tokens) with
+    respect to the logits, fp32 [t, n_experts] (tq4_moe_router_backward).  Either
+    part may be left out; `out` may not overlap an input."""
+    t, e, topk = _router_args(logits, topk_ids, score)
+    dev = logits.device
+    if dgates is not None:
+        _arg_on(dgates, "dgates", torch.float32, dev)
+        _require(tuple(dgates.shape) == (t, topk), "dgates must be [t, topk]")
+    _require((counts is None) == (tokens is None) and (counts is None) == (dloss is None),
+             "counts, tokens and dloss go together")
+    if counts is not None:
+        _arg_on(counts, "counts", torch.int32, dev)
+        _require(tuple(counts.shape) == (e,), "counts must be [n_experts]")
+        _arg_on(tokens, "tokens", torch.int32, dev)
+        _arg_on(dloss, "dloss", torch.float32, dev)
+        _require(tokens.numel() == 1 and dloss.numel() == 1, "tokens and dloss must be one value")
+    if out is None:
+        out = torch.empty((t, e), dtype=torch.float32, device=dev)
+    else:
+        _arg_on(out, "out", torch.float32, dev)
+        _require(tuple(out.shape) == (t, e), "out must be [t, n_experts]")
+    _call("tq4_moe_router_backward", dev, logits.data_ptr(), t, e, topk_ids.data_ptr(), topk,
+          SCORES[score], _ptr(dgates), int(renormalize), float(scale), _ptr(counts),
+          _ptr(tokens), _ptr(dloss), out.data_ptr())
+    return out
+
+
 def read_probe(buf: torch.Tensor, sink: torch.Tensor) -> None:
     """One streaming read of a whole device buffer (tq4_read_probe), for timing."""
     _require(buf.is_cuda and buf.is_contiguous(), "buf must be a contiguous device tensor")

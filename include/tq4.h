@@ -435,6 +435,134 @@ int tq4_moe_grouped_int8(const uint16_t *x_bf16, int64_t t, int64_t k, const int
                          const uint8_t *w1_cache, int64_t n1, const uint8_t *w2_cache, float *out,
                          void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- MXFP4 products ------------------------------------------------------
+ * The layers on 4-bit floating-point operands (model card, Running it: the
+ * projections that every forward runs; Help wanted: a resident copy that no
+ * forward decodes): 4.25 bits per weight, activations quantized per call.
+ *
+ * 32 consecutive k of a row share a scale 2^e stored as the E8M0 byte e + 127;
+ * with a = max|v| of the block, e is the smallest integer from -127 with a <
+ * 7 * 2^e.  A value is held as the OCP e2m1 code (bit 3 sign, bits 2-1
+ * exponent, bit 0 mantissa: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) nearest to
+ * v / 2^e, ties to the even code, 6 at most; the sign is kept, also of zero.  A
+ * block holding a NaN or an infinity has scale byte 255 (NaN) and zero codes.
+ * Two codes a byte, the lower k in the low half.  Rows are padded to kp = k
+ * rounded up to a multiple of 128 with zero codes and zero scale bytes, which
+ * add nothing to a product.  A cache of an [n, k] matrix is the codes
+ * [n][kp/2] followed by the scale bytes [n][kp/32].  Sizes: rows up to 2^31 - 1,
+ * k a multiple of 32 up to 2^20. */
+
+/* Bytes of the MXFP4 cache of an [n, k] matrix: n * kp / 2 + n * kp / 32 (0 if
+ * the sizes are invalid or empty). */
+size_t tq4_mxfp4_cache_size(int64_t n, int64_t k);
+
+/* Build the cache from a packed [n][k/32][20] matrix (device, 4-byte
+ * aligned): the decoded weights W_hat (rotation undone) held as above, the
+ * decoding and the choices in fp64.  cache: device, 16-byte aligned,
+ * tq4_mxfp4_cache_size bytes.  Offline, like tq4_pack.  Errors: TQ4_E_NULL,
+ * TQ4_E_SHAPE, TQ4_E_ALIGN, TQ4_E_DEVICE.  n == 0 or k == 0 is a no-op. */
+int tq4_mxfp4_cache(const uint8_t *packed, int64_t n, int64_t k, uint32_t sign_bits,
+                    uint8_t *cache, void *stream);
+
+/* The same from BF16 weights [n, k] (device, 16-byte aligned; the form the
+ * checkpoint ships in).  Errors as tq4_mxfp4_cache. */
+int tq4_mxfp4_cache_bf16(const uint16_t *w_bf16, int64_t n, int64_t k, uint8_t *cache,
+                         void *stream);
+
+/* Quantize bf16 activations [m, k] (device, 16-byte aligned) as above: codes
+ * [m][kp/2] (device, 16-byte aligned) and scale bytes [m][kp/32] (device,
+ * 4-byte aligned).  Errors as tq4_mxfp4_cache; m == 0 or k == 0 is a no-op. */
+int tq4_act_mxfp4(const uint16_t *x_bf16, int64_t m, int64_t k, uint8_t *codes, uint8_t *scales,
+                  void *stream);
+
+/* The values that codes [m][kp/2] (device, 16-byte aligned) and scale bytes
+ * [m][kp/32] (device, 4-byte aligned) stand for, as bf16 [m, k] (device,
+ * 16-byte aligned): exact, or infinite where the scale puts a value past bf16's
+ * largest; NaN in blocks of scale byte 255.  For tq4_act_mxfp4's output and for
+ * the two parts of a cache.  Errors as tq4_mxfp4_cache. */
+int tq4_mxfp4_values(const uint8_t *codes, const uint8_t *scales, int64_t m, int64_t k,
+                     uint16_t *values_bf16, void *stream);
+
+/* Workspace bytes for tq4_linear_mxfp4 and its epilogue forms (the quantized
+ * activations; 0 for m <= 16, whose rows the product quantizes itself). */
+size_t tq4_linear_mxfp4_workspace_size(int64_t m, int64_t k, int64_t n);
+
+/* y[m, n] = sum_k xq[m, k] wq[n, k], both operands at the values of their MXFP4
+ * codes: x quantized per call, the weights from a cache built by
+ * tq4_mxfp4_cache or tq4_mxfp4_cache_bf16.  The product runs on the
+ * block-scaled fp4 MFMA with fp32 accumulation, deterministic.  Every product is a
+ * multiple of u = 2^-2 times the smallest product of two scales that meet; while
+ * the sum of the magnitudes stays below 2^24 u (scales of a row within a few binades,
+ * as of activations and weights in use) the result is the exact sum and does not
+ * depend on m.  Rows of x that hold a NaN or an infinity, and such rows of the
+ * weights, give NaN.
+ *   x_bf16 : [m, k] bf16 bit patterns, device, 16-byte aligned
+ *   cache  : for this [n, k], device, 16-byte aligned
+ *   y      : [m, n] fp32, device, 4-byte aligned, overwritten
+ *   workspace : tq4_linear_mxfp4_workspace_size(m, k, n) bytes, 256-byte
+ *               aligned (may be NULL when that size is 0)
+ * Errors: as tq4_linear, plus TQ4_E_SHAPE for m or n above 2^24 and for a y
+ * that overlaps x.  m == 0 or n == 0 is a no-op; k == 0 writes zeros. */
+int tq4_linear_mxfp4(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache, int64_t n,
+                     float *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* tq4_linear_mxfp4 with the additive tail of tq4_linear_epilogue at the final
+ * store: + bias[n], then + residual[m, n], in fp32; either may be NULL, and
+ * the residual may be y itself.  With both NULL the result equals
+ * tq4_linear_mxfp4's bit for bit.  Errors as tq4_linear_epilogue; k == 0 writes
+ * bias + residual. */
+int tq4_linear_mxfp4_epilogue(const uint16_t *x_bf16, int64_t m, int64_t k, const uint8_t *cache,
+                              int64_t n, const float *bias, const float *residual, float *y,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same with a bf16 residual stream and bf16 output: the bf16 rounding of
+ * tq4_linear_mxfp4_epilogue's fp32 result, bit for bit.  Arguments and errors
+ * as tq4_linear_epilogue_bf16. */
+int tq4_linear_mxfp4_epilogue_bf16(const uint16_t *x_bf16, int64_t m, int64_t k,
+                                   const uint8_t *cache, int64_t n, const float *bias,
+                                   const uint16_t *residual_bf16, uint16_t *y_bf16,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* tq4_linear_mxfp4 with the activations already quantized by tq4_act_mxfp4
+ * (x_codes [m][kp/2], device, 16-byte aligned; x_scales [m][kp/32], device,
+ * 4-byte aligned), so one quantization can serve several projections of the
+ * same input.  Codes and scale bytes behind k must be zero, as tq4_act_mxfp4 leaves
+ * them.  No workspace.  Errors as tq4_linear_mxfp4. */
+int tq4_linear_mxfp4_quantized(const uint8_t *x_codes, const uint8_t *x_scales, int64_t m,
+                               int64_t k, const uint8_t *cache, int64_t n, float *y,
+                               void *stream);
+
+/* Workspace bytes tq4_moe_grouped_mxfp4 needs (0 if the sizes are invalid). */
+size_t tq4_moe_grouped_mxfp4_workspace_size(int64_t t, int32_t topk, int32_t n_experts, int64_t n1,
+                                            int64_t k);
+
+/* The MoE layer of tq4_moe_grouped on MXFP4 expert caches (model card, Running
+ * it: the sync-free MoE; The model underneath: 128 experts, top-6):
+ *   out[t, :] = sum_j topk_w[t, j] * dq(q(h_tj)) . dq(W2_e)^T,
+ *   h_tj = relu(u_tj)^2,  u_tj = dq(q(x[t, :])) . dq(W1_e)^T,  e = topk_ids[t, j],
+ * where q is the quantization of tq4_act_mxfp4 (on h: the fp32 square of the fp32
+ * u) and dq its value; ids outside [0, n_experts) contribute nothing (a token
+ * without any gets zeros).  Sums as tq4_linear_mxfp4; NaN rows stay NaN.
+ *   x_bf16   : [t, k] bf16 bit patterns, device, 16-byte aligned
+ *   topk_ids : [t, topk] int32, device;  topk_w : [t, topk] fp32, device
+ *   w1_cache : tq4_mxfp4_cache of the experts' up projections stacked as one
+ *              [n_experts * n1, k] matrix (expert e = rows e*n1 ...), device,
+ *              16-byte aligned
+ *   w2_cache : the same for the down projections, [n_experts * k, n1]
+ *   out      : [t, k] fp32, device, 16-byte aligned, overwritten
+ *   workspace: tq4_moe_grouped_mxfp4_workspace_size(...) bytes, device,
+ *              256-byte aligned, no initial contents required
+ * Steps: activation quantization, bucketing, grouped up projection whose epilogue
+ * squares and quantizes the hidden values, grouped down projection, and the
+ * per-token weighted sum in slot order (fp32).  Deterministic.  Errors: as
+ * tq4_moe_grouped, plus TQ4_E_SHAPE when t * kp / 2 or t * topk * n1p / 2 reach 2^31
+ * (kp, n1p: k, n1 padded to 128), when k or n1 exceed 2^20, or when the pairs may
+ * need 65536 row tiles or more. */
+int tq4_moe_grouped_mxfp4(const uint16_t *x_bf16, int64_t t, int64_t k, const int32_t *topk_ids,
+                          const float *topk_w, int32_t topk, int32_t n_experts,
+                          const uint8_t *w1_cache, int64_t n1, const uint8_t *w2_cache, float *out,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 /* Stable bucketing of the t*topk (token, slot) pairs by expert, the routing
  * step of the sync-free MoE (model card, Running it; 128 experts, top-6 in
  * The model underneath).  Pair p = token * topk + slot.
@@ -537,6 +665,56 @@ int tq4_moe_router_scored(const float *logits, int64_t t, int32_t n_experts, int
                           int score, const float *bias, int32_t n_groups, int32_t topk_groups,
                           int renormalize, float scale, int32_t *topk_ids, float *topk_w,
                           void *stream);
+
+/* Workspace bytes tq4_moe_balance needs (0 if the sizes are invalid). */
+size_t tq4_moe_balance_workspace_size(int64_t t, int32_t n_experts);
+
+/* The router's balance statistics and loss, for setting tq4_moe_router_scored's
+ * bias and for training the router (model card, The model underneath: the
+ * 128-expert, top-6 layer; its router stays unquantized).  With p_te the scores of
+ * tq4_moe_router_scored (0 for an expert whose logit is -infinity or NaN; a logit of
+ * +infinity counts as the largest finite value), q_te = p_te / sum_i p_ti, and the
+ * live tokens those with an id in [0, n_experts):
+ *   counts[e]  = pairs (token, slot) with topk_ids[t, j] == e
+ *   tokens[0]  = live tokens T
+ *   mean_p[e]  = (1 / T) sum over live t of q_te          (0 if T == 0)
+ *   loss[0]    = E * sum_e (counts[e] / sum counts) * mean_p[e],  E = n_experts
+ * Rows routed nowhere, such as those that fill up a batch, take no part.  An even
+ * router has loss 1.  Scores are fp32, sums over tokens fp64 beyond a lane's few;
+ * deterministic.
+ *   logits   : [t, n_experts] fp32, device;  topk_ids : [t, topk] int32, device
+ *   loss, tokens : one value each, counts, mean_p : [n_experts], device, overwritten
+ *   workspace: tq4_moe_balance_workspace_size(t, n_experts) bytes, device,
+ *              256-byte aligned, no initial contents required
+ * Errors: TQ4_E_SHAPE (t < 0, t * topk >= 2^31, n_experts outside 1..512, topk
+ * outside 1..n_experts, an unknown score), TQ4_E_NULL, TQ4_E_ALIGN (4-byte),
+ * TQ4_E_WORKSPACE, TQ4_E_DEVICE.  t == 0 writes zeros. */
+int tq4_moe_balance(const float *logits, int64_t t, int32_t n_experts, const int32_t *topk_ids,
+                    int32_t topk, int score, float *loss, int32_t *counts, int32_t *tokens,
+                    float *mean_p, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The gradient of the router's outputs with respect to its logits:
+ *   dlogits[t, e] = sum_j dgates[t, j] * d topk_w[t, j] / d logits[t, e]
+ *                   + dloss[0] * d loss / d logits[t, e]
+ * for the weights topk_w that tq4_moe_router_scored gives to these topk_ids with
+ * this score, renormalize and scale (tq4_moe_router: softmax, 0, 1), and the loss
+ * of tq4_moe_balance, which depends on the logits through mean_p (the counts are
+ * constants).  The choice of experts has no gradient.  Slots with an id outside
+ * [0, n_experts) contribute nothing; slots of one expert add up; experts that are
+ * switched off have gradient 0.
+ *   dgates : [t, topk] fp32, device, or NULL (no gradient from the gates)
+ *   counts, tokens : tq4_moe_balance's for these ids, and dloss : one fp32 value,
+ *            device; all three, or all NULL (no gradient from the loss)
+ *   dlogits : [t, n_experts] fp32, device, overwritten; may not overlap an input
+ * fp32, deterministic.  Errors: TQ4_E_SHAPE as tq4_moe_balance, and for a dlogits
+ * that overlaps the logits, ids or dgates; TQ4_E_NULL (also for some but not all of
+ * counts, tokens and dloss), TQ4_E_ALIGN (4-byte), TQ4_E_DEVICE.  t == 0 is a
+ * no-op. */
+int tq4_moe_router_backward(const float *logits, int64_t t, int32_t n_experts,
+                            const int32_t *topk_ids, int32_t topk, int score, const float *dgates,
+                            int renormalize, float scale, const int32_t *counts,
+                            const int32_t *tokens, const float *dloss, float *dlogits,
+                            void *stream);
 
 /* Workspace bytes tq4_moe_block needs (0 if the sizes are invalid). */
 size_t tq4_moe_block_workspace_size(int64_t t, int32_t topk, int32_t n_experts,
