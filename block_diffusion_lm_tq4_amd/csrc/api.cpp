@@ -1187,10 +1187,13 @@ int tq4_moe_grouped_mxfp4(const uint16_t *x_bf16, int64_t t, int64_t k, const in
   const uint8_t *w1_scales = w1_cache + fp4_codes_bytes(n_experts * n1, k);
   const uint8_t *w2_scales = w2_cache + fp4_codes_bytes(n_experts * k, n1);
   hipStream_t s = as_stream(stream);
-  hipError_t e = tq4::launch_act_mxfp4(x_bf16, t, k, xq, xs, s);
-  if (e == hipSuccess)
-    e = tq4::launch_route(topk_ids, pairs, topk, n_experts, counts, offsets, perm, inv, tiles,
-                          meta, l.tile_rows, nullptr, s);
+  if (tq4::mxfp4_moe_direct_fits(t, topk))
+    return device_status(tq4::launch_moe_mxfp4_direct(
+        x_bf16, t, k, topk_ids, topk_w, topk, n_experts, w1_cache, w1_scales, n1, w2_cache,
+        w2_scales, hq, hs, out, s));
+  hipError_t e =
+      tq4::launch_moe_mxfp4_prepare(x_bf16, t, k, topk_ids, topk, n_experts, counts, offsets, perm,
+                                    inv, tiles, meta, l.tile_rows, xq, xs, s);
   if (e == hipSuccess)
     e = tq4::launch_moe_mxfp4(0, l.tile_rows, xq, xs, t, k, perm, topk, w1_cache, w1_scales, n1,
                               tiles, meta, l.max_tiles, nullptr, hq, hs, s);
@@ -1215,7 +1218,7 @@ bool balance_sizes_ok(int64_t t, int32_t n_experts, int32_t topk, int score) {
 
 size_t tq4_moe_balance_workspace_size(int64_t t, int32_t n_experts) {
   if (t < 0 || t > INT32_MAX || n_experts < 1 || n_experts > 512) return 0;
-  return align_up(static_cast<size_t>(tq4::balance_groups(t)) * (2 * n_experts + 1) * 4);
+  return align_up(tq4::balance_scratch(t, n_experts));
 }
 
 int tq4_moe_balance(const float *logits, int64_t t, int32_t n_experts, const int32_t *topk_ids,

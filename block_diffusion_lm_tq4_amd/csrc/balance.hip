@@ -29,9 +29,7 @@ namespace {
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 256;
-constexpr int kLanes = 16;                 // lanes of a token
-constexpr int kTokens = kThreads / kLanes; // tokens of a workgroup at a time
+constexpr int kLanes = 16;  // lanes of a token
 constexpr int kMaxE = 512;
 constexpr float kOff = -__builtin_inff();
 
@@ -58,14 +56,16 @@ __device__ inline float row_sum(float v) {
 }
 
 // e^x for x <= 0 with a relative error of about 2 ulp: 2^t of the rounded product t = x
-// log2(e), times the first two terms of e^r for what its rounding left.
+// log2(e), times the first two terms of e^r for what its rounding left.  0 from -104 on,
+// past fp32's smallest number, and for NaN (of two infinities).
 __device__ inline float exp_neg(float x) {
   constexpr float kLog2e = 0x1.715476p+0f, kLow = 0x1.4ae0cp-26f;  // log2(e) in two parts
   constexpr float kLn2 = 0x1.62e43p-1f;
+  x = __builtin_fmaxf(x, -104.f);
   const float t = x * kLog2e;
-  const float r = __builtin_fmaf(x, kLow, __builtin_fmaf(x, kLog2e, -t)) * kLn2;
+  const float r = __builtin_fmaf(x, kLow, __builtin_fmaf(x, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t);
-  return t > -150.f ? __builtin_fmaf(e, r, e) : 0.f;  // also for x = -inf
+  return __builtin_fmaf(e, r * kLn2, e);
 }
 
 // A logit as the scores take it: off at -inf and NaN, finite above.
@@ -80,7 +80,6 @@ struct Row {
   float top;
 
   __device__ void load(const float *row, int n_experts, int lane) {
-    top = kOff;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = 64 * i + 4 * lane;
@@ -93,31 +92,43 @@ struct Row {
 #pragma unroll
         for (int v = 0; v < 4; ++v) l[i][v] = e + v < n_experts ? row[e + v] : kOff;
       }
+    }
+  }
+
+  __device__ void clean() {
+    top = kOff;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         l[i][v] = usable(l[i][v]);
         top = __builtin_fmaxf(top, l[i][v]);
       }
-    }
     top = row_max(top);
   }
 };
 
 // A score relative to e^top (softmax) or to e^min(top, 0) (sigmoid), and 1 - p of the
-// sigmoid.
+// sigmoid.  With z = e^-|l| the sigmoid is 1 / (1 + z) or z / (1 + z) and 1 - p the other
+// one; only where every logit is negative does the base need an exponential of its own.
 template <bool SIGMOID>
 __device__ inline float score(float l, float top, float &rest) {
   if constexpr (SIGMOID) {
-    const float inv = __builtin_amdgcn_rcpf(1.f + exp_neg(-__builtin_fabsf(l)));
-    rest = exp_neg(-__builtin_fmaxf(l, 0.f)) * inv;
-    return exp_neg(__builtin_fminf(l, 0.f) - __builtin_fminf(top, 0.f)) * inv;
+    const float z = exp_neg(-__builtin_fabsf(l));
+    const float inv = __builtin_amdgcn_rcpf(1.f + z);
+    const bool pos = l >= 0.f;
+    rest = (pos ? z : 1.f) * inv;
+    const float base = top >= 0.f ? (pos ? 1.f : z) : exp_neg(l - top);
+    return base * inv;
   } else {
     rest = 1.f;
     return exp_neg(l - top);
   }
 }
 
-// Scores of a whole row and 1 / their sum (0 for a row without experts).
+// Scores of a whole row and 1 / their sum (0 for a row without experts).  (An expert that
+// is off has l = -inf, hence e^-inf = 0 throughout; a row of only such ones has the base
+// -inf too and is left out.)
 template <bool SIGMOID, int NV, bool VEC>
 __device__ inline float row_scores(const Row<NV, VEC> &row, float (&p)[NV][4],
                                    float (&rest)[NV][4]) {
@@ -126,8 +137,7 @@ __device__ inline float row_scores(const Row<NV, VEC> &row, float (&p)[NV][4],
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const float s = score<SIGMOID>(row.l[i][v], row.top, rest[i][v]);
-      p[i][v] = row.l[i][v] > kOff ? s : 0.f;
+      p[i][v] = score<SIGMOID>(row.l[i][v], row.top, rest[i][v]);
       sum += p[i][v];
     }
   sum = row_sum(sum);
@@ -136,43 +146,109 @@ __device__ inline float row_scores(const Row<NV, VEC> &row, float (&p)[NV][4],
 
 __device__ inline bool routed(int id, int n_experts) { return id >= 0 && id < n_experts; }
 
-// Whether the token has an id in range (all lanes of the token agree).
-__device__ inline bool row_live(const int32_t *ids, int topk, int n_experts, int lane) {
-  float any = 0.f;
-  for (int j = lane; j < topk; j += kLanes) any = routed(ids[j], n_experts) ? 1.f : any;
-  return row_max(any) > 0.f;
-}
-
 // ---- counts, mean probabilities, loss ----------------------------------------
 
-// A workgroup's share of the tokens: its sums of q and its counts go to scratch
-// ([groups][E] fp32, [groups][E] int32, [groups] int32).
-template <bool SIGMOID, int NV, bool VEC>
-__global__ __launch_bounds__(kThreads) void balance_sums_kernel(BalanceArgs a, float *part_p,
-                                                                int32_t *part_c, int32_t *part_t) {
-  __shared__ float sums[kTokens][64 * NV];
+constexpr int kSumThreads = 1024;
+constexpr int kSumTokens = kSumThreads / kLanes;  // of a workgroup at a time
+constexpr int kMaxGroups = 256;                   // one per compute unit
+
+struct BalanceOut {
+  float *loss, *mean_p;
+  int32_t *counts, *tokens;
+};
+
+// The experts of one workgroup of the second launch.  Its sums of a group are one cache
+// line (a compute unit has few misses under way: slices of 64 experts, whose sums and
+// counts were two lines each, took 15 us for 256 groups of 256 experts).
+constexpr int kSlice = 16;
+
+// A group's sums in scratch, and what the slices of experts add up.
+struct BalanceParts {
+  uint32_t *sums;  // [slices][groups][kSlice sums of q, then kSlice counts]
+  int32_t *t;      // [groups]
+  double *dot;     // [slices]: sum of mean * count
+  int64_t *pairs;  // [slices]
+  uint32_t *done;  // slices that are through (cleared by the sums' launch)
+};
+
+// Sums over a workgroup, in wave order; every thread calls, thread 0 has the results.
+__device__ inline void group_sums(double &d, int64_t &n, double *lds_d, int64_t *lds_n) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) {
+    d += __shfl_xor(d, x);
+    n += __shfl_xor(n, x);
+  }
+  if (tid % 64 == 0) {
+    lds_d[tid / 64] = d;
+    lds_n[tid / 64] = n;
+  }
+  __syncthreads();
+  if (tid == 0)
+    for (int w = 1; w < kSumThreads / 64; ++w) {
+      d += lds_d[w];
+      n += lds_n[w];
+    }
+}
+
+__device__ inline float balance_loss(int n_experts, double dot, int64_t pairs) {
+  return pairs > 0 ? static_cast<float>(n_experts * dot / static_cast<double>(pairs)) : 0.f;
+}
+
+// One expert's totals to the outputs; adds its share of the loss.
+__device__ inline void balance_expert(const BalanceOut &o, int e, double p, int32_t c,
+                                      int32_t live, double &dot, int64_t &pairs) {
+  const double mean = live > 0 ? p / static_cast<double>(live) : 0.0;
+  o.counts[e] = c;
+  o.mean_p[e] = static_cast<float>(mean);
+  dot += mean * static_cast<double>(c);
+  pairs += c;
+}
+
+// A workgroup's share of the tokens.  With ONE workgroup its sums are the result, else its
+// sums of q and its counts go to scratch.  A token's row, and the ids, are fetched a round ahead where the
+// registers hold two rows.
+template <bool SIGMOID, int NV, bool VEC, bool ONE>
+__global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a, BalanceOut o,
+                                                                   BalanceParts parts) {
+  constexpr int kWaves = kSumThreads / 64;
+  __shared__ float sums[kWaves][64 * NV];
   __shared__ int32_t hist[64 * NV];
   __shared__ int32_t tokens;
+  __shared__ double dot[kWaves];
+  __shared__ int64_t all[kWaves];
   const int tid = threadIdx.x;
   const int lane = tid % kLanes, group = tid / kLanes;
-  for (int e = tid; e < 64 * NV; e += kThreads) hist[e] = 0;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSumTokens + group;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kSumTokens;
+  constexpr bool kAhead = NV <= 4;
+  Row<NV, VEC> next;
+  int next_id = -1;
+  auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+    next.load(a.logits + t * a.n_experts, a.n_experts, lane);
+    if (lane < a.topk) next_id = a.ids[t * a.topk + lane];
+  };
+  if (kAhead && first < a.t) fetch(first);
+  for (int e = tid; e < 64 * NV; e += kSumThreads) hist[e] = 0;
   if (tid == 0) tokens = 0;
   __syncthreads();
   float acc[NV][4] = {};
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + group; t < a.t;
-       t += static_cast<int64_t>(gridDim.x) * kTokens) {
-    const int32_t *ids = a.ids + t * a.topk;
-    bool any = false;
-    for (int j = lane; j < a.topk; j += kLanes) {
-      const int id = ids[j];
+  for (int64_t t = first; t < a.t; t += stride) {
+    if (!kAhead) fetch(t);
+    Row<NV, VEC> row = next;
+    const int own_id = next_id;
+    if (kAhead && t + stride < a.t) fetch(t + stride);
+    bool any = routed(own_id, a.n_experts);
+    if (any) atomicAdd(&hist[own_id], 1);
+    for (int j = lane + kLanes; j < a.topk; j += kLanes) {
+      const int id = a.ids[t * a.topk + j];
       if (!routed(id, a.n_experts)) continue;
       atomicAdd(&hist[id], 1);
       any = true;
     }
     if (row_max(any ? 1.f : 0.f) == 0.f) continue;  // routed nowhere
     if (lane == 0) atomicAdd(&tokens, 1);
-    Row<NV, VEC> row;
-    row.load(a.logits + t * a.n_experts, a.n_experts, lane);
+    row.clean();
     float p[NV][4], rest[NV][4];
     const float inv = row_scores<SIGMOID, NV, VEC>(row, p, rest);
 #pragma unroll
@@ -180,131 +256,175 @@ __global__ __launch_bounds__(kThreads) void balance_sums_kernel(BalanceArgs a, f
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[i][v] += p[i][v] * inv;
   }
+  // the wave's four tokens, then the waves in order
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) sums[group][64 * i + 4 * lane + v] = acc[i][v];
+    for (int v = 0; v < 4; ++v) {
+      float s = acc[i][v];
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (tid % 64 < kLanes) sums[tid / 64][64 * i + 4 * lane + v] = s;
+    }
   __syncthreads();
-  for (int e = tid; e < a.n_experts; e += kThreads) {
-    float s = 0.f;
-#pragma unroll
-    for (int g = 0; g < kTokens; ++g) s += sums[g][e];
-    part_p[static_cast<int64_t>(blockIdx.x) * a.n_experts + e] = s;
-    part_c[static_cast<int64_t>(blockIdx.x) * a.n_experts + e] = hist[e];
-  }
-  if (tid == 0) part_t[blockIdx.x] = tokens;
-}
-
-constexpr int kFinalThreads = 1024;
-
-// One workgroup adds the groups' sums in a fixed order, fp64.
-__global__ __launch_bounds__(kFinalThreads) void balance_loss_kernel(
-    const float *__restrict__ part_p, const int32_t *__restrict__ part_c,
-    const int32_t *__restrict__ part_t, int groups, int n_experts, float *loss, int32_t *counts,
-    int32_t *tokens, float *mean_p) {
-  __shared__ double sp[kFinalThreads];
-  __shared__ int32_t sc[kFinalThreads];
-  __shared__ int32_t st;
-  __shared__ double dot[kFinalThreads / 64];
-  __shared__ int64_t all[kFinalThreads / 64];
-  const int tid = threadIdx.x;
-  int cols = 1;
-  while (cols < n_experts) cols *= 2;
-  const int parts = kFinalThreads / cols;
-  const int e = tid % cols, part = tid / cols;
   double p = 0.0;
   int32_t c = 0;
-  if (e < n_experts)
-    for (int g = part; g < groups; g += parts) {
-      p += static_cast<double>(part_p[g * n_experts + e]);
-      c += part_c[g * n_experts + e];
+  if (tid < a.n_experts) {
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) p += static_cast<double>(sums[w][tid]);
+    c = hist[tid];
+  }
+  if constexpr (ONE) {
+    double d = 0.0;
+    int64_t n = 0;
+    if (tid < a.n_experts) balance_expert(o, tid, p, c, tokens, d, n);
+    group_sums(d, n, dot, all);
+    if (tid == 0) {
+      *o.loss = balance_loss(a.n_experts, d, n);
+      *o.tokens = tokens;
     }
-  sp[tid] = p;
-  sc[tid] = c;
+  } else {
+    if (tid < a.n_experts) {
+      uint32_t *to = parts.sums + ((tid / kSlice) * gridDim.x + blockIdx.x) * (2 * kSlice) +
+                     tid % kSlice;
+      to[0] = __float_as_uint(static_cast<float>(p));
+      to[kSlice] = static_cast<uint32_t>(c);
+    }
+    if (tid == 0) {
+      parts.t[blockIdx.x] = tokens;
+      if (blockIdx.x == 0) *parts.done = 0;
+    }
+  }
+}
+
+// A workgroup adds the groups' sums of its slice in a fixed order, fp64: thread e + 16 i
+// takes groups i, i + 64, ... of expert e, all on their way at once.  The last workgroup
+// through adds the slices' shares of the loss, in order.
+__global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts parts, int groups,
+                                                                   int n_experts, BalanceOut o) {
+  constexpr int kParts = kSumThreads / kSlice;
+  constexpr int kAhead = kMaxGroups / kParts;
+  constexpr int kWaves = kSumThreads / 64;
+  __shared__ double sp[kWaves][kSlice];
+  __shared__ int32_t sc[kWaves][kSlice];
+  __shared__ int32_t st;
+  __shared__ double dot[kSumThreads / 64];
+  __shared__ int64_t all[kSumThreads / 64];
+  const int tid = threadIdx.x;
+  const int col = tid % kSlice, part = tid / kSlice;
+  const int e = static_cast<int>(blockIdx.x) * kSlice + col;
+  float dp[kAhead];
+  int32_t dc[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int g = part + kParts * i;
+    const bool in = g < groups && e < n_experts;
+    const uint32_t *from =
+        parts.sums + (static_cast<int>(blockIdx.x) * groups + g) * (2 * kSlice) + col;
+    dp[i] = in ? __uint_as_float(from[0]) : 0.f;
+    dc[i] = in ? static_cast<int32_t>(from[kSlice]) : 0;
+  }
+  const int32_t t = tid < groups ? parts.t[tid] : 0;
   if (tid == 0) st = 0;
+  double p = 0.0;
+  int32_t c = 0;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    p += static_cast<double>(dp[i]);
+    c += dc[i];
+  }
+  // the wave's four parts, then the waves in order
+#pragma unroll
+  for (int x = kSlice; x < 64; x <<= 1) {
+    p += __shfl_xor(p, x);
+    c += __shfl_xor(c, x);
+  }
+  if (tid % 64 < kSlice) {
+    sp[tid / 64][col] = p;
+    sc[tid / 64][col] = c;
+  }
   __syncthreads();
-  int32_t t = 0;
-  for (int g = tid; g < groups; g += kFinalThreads) t += part_t[g];
   if (t != 0) atomicAdd(&st, t);
   __syncthreads();
-  const int32_t live = st;
-  double part_dot = 0.0;
-  int64_t part_all = 0;
-  if (tid < n_experts) {
-    for (int q = 1; q < parts; ++q) {
-      p += sp[q * cols + e];
-      c += sc[q * cols + e];
-    }
-    const double mean = live > 0 ? p / static_cast<double>(live) : 0.0;
-    counts[e] = c;
-    mean_p[e] = static_cast<float>(mean);
-    part_dot = mean * static_cast<double>(c);
-    part_all = c;
-  }
+  double d = 0.0;
+  int64_t n = 0;
+  if (part == 0 && e < n_experts) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    part_dot += __shfl_xor(part_dot, d);
-    part_all += __shfl_xor(part_all, d);
-  }
-  if (tid % 64 == 0) {
-    dot[tid / 64] = part_dot;
-    all[tid / 64] = part_all;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    double s = 0.0;
-    int64_t n = 0;
-    for (int w = 0; w < kFinalThreads / 64; ++w) {
-      s += dot[w];
-      n += all[w];
+    for (int q = 1; q < kWaves; ++q) {
+      p += sp[q][col];
+      c += sc[q][col];
     }
-    *loss = n > 0 ? static_cast<float>(n_experts * s / static_cast<double>(n)) : 0.f;
-    *tokens = live;
+    balance_expert(o, e, p, c, st, d, n);
   }
+  group_sums(d, n, dot, all);
+  if (tid != 0) return;
+  if (blockIdx.x == 0) *o.tokens = st;
+  if (gridDim.x == 1) {
+    *o.loss = balance_loss(n_experts, d, n);
+    return;
+  }
+  parts.dot[blockIdx.x] = d;
+  parts.pairs[blockIdx.x] = n;
+  __threadfence();
+  if (atomicAdd(parts.done, 1u) + 1 < gridDim.x) return;
+  __threadfence();
+  d = 0.0;
+  n = 0;
+  for (unsigned i = 0; i < gridDim.x; ++i) {
+    d += __hip_atomic_load(parts.dot + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    n += __hip_atomic_load(parts.pairs + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  *o.loss = balance_loss(n_experts, d, n);
 }
 
 // ---- gradient ------------------------------------------------------------------
 
-// The gates' contributions of one token to `delta` (its row of LDS), and what a softmax
-// without renormalization takes from every expert (sum_j p_j a_j).  Lane j of the
-// token takes slots j, j + 16, ....
-template <bool SIGMOID>
-__device__ inline float gate_part(const RouterGradArgs &g, int64_t t, float top, float inv,
-                                  float *delta, int lane) {
-  const float *row = g.b.logits + t * g.b.n_experts;
-  const int32_t *ids = g.b.ids + t * g.b.topk;
-  const float *dw = g.dgates + t * g.b.topk;
-  const int blocks = (g.b.topk + kLanes - 1) / kLanes;
-  auto slot = [&](int b, int &id, float &l, float &d) __attribute__((always_inline)) {
-    const int j = b * kLanes + lane;
-    id = j < g.b.topk ? ids[j] : -1;
+constexpr int kThreads = 256;
+constexpr int kTokens = kThreads / kLanes;  // of a workgroup at a time
+
+// Slot j of a token as lane j % 16 sees it: its expert (-1: none), that expert's logit and
+// the gate's gradient.
+struct Slot {
+  int id;
+  float l, d;
+  __device__ void load(const RouterGradArgs &g, int64_t t, int j) {
+    id = -1;
     l = kOff;
     d = 0.f;
-    if (routed(id, g.b.n_experts)) {
-      l = usable(row[id]);
-      d = dw[j];
-    } else {
-      id = -1;
-    }
+    if (j >= g.b.topk) return;
+    const int at = g.b.ids[t * g.b.topk + j];
+    if (!routed(at, g.b.n_experts)) return;
+    id = at;
+    if (g.dgates == nullptr) return;
+    d = g.dgates[t * g.b.topk + j];
+    l = usable(g.b.logits[t * g.b.n_experts + at]);
+  }
+};
+
+// The gates' contributions of one token to `delta` (its row of LDS), and what a softmax
+// without renormalization takes from every expert (sum_j p_j a_j).  Lane j of the
+// token takes slots j, j + 16, ...; `own` is its first.
+template <bool SIGMOID>
+__device__ inline float gate_part(const RouterGradArgs &g, int64_t t, const Slot &own, float top,
+                                  float inv, float *delta, int lane) {
+  const int blocks = (g.b.topk + kLanes - 1) / kLanes;
+  auto slot = [&](int b) __attribute__((always_inline)) {
+    Slot s = own;
+    if (b > 0) s.load(g, t, b * kLanes + lane);
+    return s;
   };
   float base = top, norm = inv, mean = 0.f;
   if (g.renormalize) {  // scores relative to the largest chosen one
     base = kOff;
-    for (int b = 0; b < blocks; ++b) {
-      int id;
-      float l, d;
-      slot(b, id, l, d);
-      base = __builtin_fmaxf(base, l);
-    }
+    for (int b = 0; b < blocks; ++b) base = __builtin_fmaxf(base, slot(b).l);
     base = row_max(base);
     float sum = 0.f, dot = 0.f;
     for (int b = 0; b < blocks; ++b) {
-      int id;
-      float l, d, rest;
-      slot(b, id, l, d);
-      const float p = l > kOff ? score<SIGMOID>(l, base, rest) : 0.f;
+      const Slot s = slot(b);
+      float rest;
+      const float p = s.l > kOff ? score<SIGMOID>(s.l, base, rest) : 0.f;
       sum += p;
-      dot += p * d;
+      dot += p * s.d;
     }
     sum = row_sum(sum);
     norm = sum > 0.f ? 1.f / sum : 0.f;
@@ -315,14 +435,30 @@ __device__ inline float gate_part(const RouterGradArgs &g, int64_t t, float top,
   }
   float taken = 0.f;
   for (int b = 0; b < blocks; ++b) {
-    int id;
-    float l, d, rest = 1.f;
-    slot(b, id, l, d);
-    const float p = l > kOff ? score<SIGMOID>(l, base, rest) * norm : 0.f;
-    float add = p * (g.scale * (d - mean));
+    const Slot s = slot(b);
+    const int id = s.id;
+    float rest = 1.f;
+    const float p = s.l > kOff ? score<SIGMOID>(s.l, base, rest) * norm : 0.f;
+    float add = p * (g.scale * (s.d - mean));
     taken += add;
     if (SIGMOID) add *= rest;
-    // slots of one expert: the lowest lane adds the others', always in the same order
+    // Slots that all have experts of their own, as a router's have, add without a look at
+    // each other: a lane leaves its number at its expert and finds it there again.
+    if (b == 0) {
+      int *mark = reinterpret_cast<int *>(delta);
+      if (id >= 0) mark[id] = lane;
+      wave_lds_fence();
+      const bool alone = id < 0 || mark[id] == lane;
+      wave_lds_fence();
+      if (id >= 0) delta[id] = 0.f;
+      wave_lds_fence();
+      if (__builtin_amdgcn_ballot_w64(!alone) == 0) {
+        if (id >= 0) delta[id] = add;
+        wave_lds_fence();
+        continue;
+      }
+    }
+    // else the lowest lane of an expert adds the others', always in the same order
     float all = add;
     bool first = id >= 0;
     auto turn = [&](int oid, float o, int from) __attribute__((always_inline)) {
@@ -343,7 +479,8 @@ __device__ inline float gate_part(const RouterGradArgs &g, int64_t t, float top,
   return SIGMOID || g.renormalize ? 0.f : row_sum(taken);
 }
 
-// 16 lanes per token, 16 tokens per workgroup at a time.
+// 16 lanes per token, 16 tokens per workgroup at a time.  A token's row and slots are
+// fetched before anything waits.
 template <bool SIGMOID, int NV, bool VEC>
 __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArgs g) {
   __shared__ __attribute__((aligned(16))) float delta_all[kTokens][64 * NV];
@@ -353,42 +490,64 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
   const int lane = tid % kLanes, group = tid / kLanes;
   const int n_experts = g.b.n_experts;
   const bool has_loss = g.counts != nullptr;
+  const bool has_gates = g.dgates != nullptr;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kTokens + group;
+  Row<NV, VEC> row;
+  Slot own;
+  if (first < g.b.t) {
+    row.load(g.b.logits + first * n_experts, n_experts, lane);
+    own.load(g, first, lane);
+  }
   if (has_loss) {
-    int32_t n = 0;
-    for (int e = tid; e < n_experts; e += kThreads) n += g.counts[e];
+    constexpr int kPer = (64 * NV + kThreads - 1) / kThreads;
+    int32_t count[kPer], n = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid + kThreads * i;
+      count[i] = e < n_experts ? g.counts[e] : 0;
+      n += count[i];
+    }
+    const double tokens = *g.tokens, dloss = *g.dloss;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
     if (tid % 64 == 0) total[tid / 64] = n;
     __syncthreads();
     n = 0;
     for (int w = 0; w < kThreads / 64; ++w) n += total[w];
-    const double pairs = n, tokens = *g.tokens;
-    const double c0 = pairs > 0.0 && tokens > 0.0
-                          ? static_cast<double>(*g.dloss) * n_experts / (pairs * tokens)
-                          : 0.0;
-    for (int e = tid; e < 64 * NV; e += kThreads)
-      share[e] = e < n_experts ? static_cast<float>(c0 * g.counts[e]) : 0.f;
+    const double pairs = n;
+    const double c0 = pairs > 0.0 && tokens > 0.0 ? dloss * n_experts / (pairs * tokens) : 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid + kThreads * i;
+      if (e < 64 * NV) share[e] = static_cast<float>(c0 * count[i]);
+    }
   }
   __syncthreads();
   float *delta = delta_all[group];
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + group; t < g.b.t;
-       t += static_cast<int64_t>(gridDim.x) * kTokens) {
-    Row<NV, VEC> row;
-    row.load(g.b.logits + t * n_experts, n_experts, lane);
+  for (int64_t t = first; t < g.b.t; t += static_cast<int64_t>(gridDim.x) * kTokens) {
+    if (t > first) {
+      row.load(g.b.logits + t * n_experts, n_experts, lane);
+      own.load(g, t, lane);
+    }
+    row.clean();
     float p[NV][4], rest[NV][4];
     const float inv = row_scores<SIGMOID, NV, VEC>(row, p, rest);
     float taken = 0.f;
-    if (g.dgates != nullptr) {
+    if (has_gates) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         *reinterpret_cast<floatx4 *>(delta + 64 * i + 4 * lane) = floatx4{0.f, 0.f, 0.f, 0.f};
       wave_lds_fence();
-      taken = gate_part<SIGMOID>(g, t, row.top, inv, delta, lane);
+      taken = gate_part<SIGMOID>(g, t, own, row.top, inv, delta, lane);
     }
+    // live: an id in range in any slot
+    bool any = own.id >= 0;
+    if (has_loss)
+      for (int j = lane + kLanes; j < g.b.topk; j += kLanes)
+        any = any || routed(g.b.ids[t * g.b.topk + j], n_experts);
+    const bool live = has_loss && row_max(any ? 1.f : 0.f) > 0.f;
     floatx4 c[NV];
     float dot = 0.f;
-    const bool live =
-        has_loss && row_live(g.b.ids + t * g.b.topk, g.b.topk, n_experts, lane);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       c[i] = live ? *reinterpret_cast<const floatx4 *>(share + 64 * i + 4 * lane)
@@ -404,7 +563,7 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
     for (int i = 0; i < NV; ++i) {
       const int e = 64 * i + 4 * lane;
       floatx4 d = {0.f, 0.f, 0.f, 0.f};
-      if (g.dgates != nullptr) d = *reinterpret_cast<const floatx4 *>(delta + e);
+      if (has_gates) d = *reinterpret_cast<const floatx4 *>(delta + e);
 #pragma unroll
       for (int v = 0; v < 4; ++v) d[v] += p[i][v] * rest[i][v] * (c[i][v] - dot);
       float *out = g.dlogits + t * n_experts + e;
@@ -440,31 +599,61 @@ void by_experts(int n_experts, bool vec, F f) {
 
 }  // namespace
 
-int balance_groups(int64_t t) {
-  const int64_t groups = (t + 4 * kTokens - 1) / (4 * kTokens);
-  return static_cast<int>(groups < 1 ? 1 : (groups < 256 ? groups : 256));
+static int balance_groups(int64_t t) {
+  if (t <= 4 * kSumTokens) return 1;
+  const int64_t groups = (t + kSumTokens - 1) / kSumTokens;
+  return static_cast<int>(groups < kMaxGroups ? groups : kMaxGroups);
+}
+
+namespace {
+
+// Scratch: the slices' shares first (16 bytes each), then the groups' sums.
+constexpr size_t kShares = (16 * (kMaxE / kSlice) + 16 + 127) / 128 * 128;
+
+}  // namespace
+
+size_t balance_scratch(int64_t t, int32_t n_experts) {
+  const size_t groups = static_cast<size_t>(balance_groups(t));
+  const size_t slices = (static_cast<size_t>(n_experts) + kSlice - 1) / kSlice;
+  return groups > 1 ? kShares + groups * (2 * kSlice * slices + 1) * 4 : 0;
 }
 
 hipError_t launch_moe_balance(const BalanceArgs &a, float *loss, int32_t *counts, int32_t *tokens,
                               float *mean_p, void *scratch, hipStream_t s) {
   if (a.n_experts < 1 || a.n_experts > kMaxE) return hipErrorInvalidValue;
   const int groups = balance_groups(a.t);
-  float *part_p = static_cast<float *>(scratch);
-  int32_t *part_c = reinterpret_cast<int32_t *>(part_p + groups * a.n_experts);
-  int32_t *part_t = part_c + groups * a.n_experts;
+  const BalanceOut out{loss, mean_p, counts, tokens};
+  BalanceParts parts{};
+  if (groups > 1) {
+    char *at = static_cast<char *>(scratch);
+    parts.dot = reinterpret_cast<double *>(at);
+    parts.pairs = reinterpret_cast<int64_t *>(at + 8 * (kMaxE / kSlice));
+    parts.done = reinterpret_cast<uint32_t *>(at + 16 * (kMaxE / kSlice));
+    parts.sums = reinterpret_cast<uint32_t *>(at + kShares);
+    parts.t = reinterpret_cast<int32_t *>(parts.sums) +
+              static_cast<int64_t>(groups) * ((a.n_experts + kSlice - 1) / kSlice) * (2 * kSlice);
+  }
   const bool vec = a.n_experts % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
   by_experts(a.n_experts, vec, [&](auto nv, auto v) {
+    auto launch = [&](auto sigmoid, auto one) {
+      hipLaunchKernelGGL((balance_sums_kernel<sigmoid.value, nv.value, v.value, one.value>),
+                         dim3(groups), dim3(kSumThreads), 0, s, a, out, parts);
+    };
+    auto with = [&](auto sigmoid) {
+      if (groups == 1)
+        launch(sigmoid, std::true_type{});
+      else
+        launch(sigmoid, std::false_type{});
+    };
     if (a.sigmoid)
-      hipLaunchKernelGGL((balance_sums_kernel<true, nv.value, v.value>), dim3(groups),
-                         dim3(kThreads), 0, s, a, part_p, part_c, part_t);
+      with(std::true_type{});
     else
-      hipLaunchKernelGGL((balance_sums_kernel<false, nv.value, v.value>), dim3(groups),
-                         dim3(kThreads), 0, s, a, part_p, part_c, part_t);
+      with(std::false_type{});
   });
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(kFinalThreads), 0, s, part_p, part_c,
-                     part_t, groups, a.n_experts, loss, counts, tokens, mean_p);
+  if (e != hipSuccess || groups == 1) return e;
+  hipLaunchKernelGGL(balance_loss_kernel, dim3((a.n_experts + kSlice - 1) / kSlice),
+                     dim3(kSumThreads), 0, s, parts, groups, a.n_experts, out);
   return hipGetLastError();
 }
 

@@ -25,6 +25,13 @@ bool mxfp4_direct_fits(int64_t m);
 hipError_t launch_linear_mxfp4_direct(const uint16_t *x, int64_t m, int64_t k, const uint8_t *wq,
                                       const uint8_t *ws, int64_t n, const Tail &tail, void *y,
                                       hipStream_t s);
+// The MoE layer's first step: launch_route's outputs for the pairs, and x's codes and
+// scale bytes.
+hipError_t launch_moe_mxfp4_prepare(const uint16_t *x, int64_t t, int64_t k, const int32_t *ids,
+                                    int32_t topk, int32_t n_experts, int32_t *counts,
+                                    int32_t *offsets, int32_t *perm, int32_t *inv, MoETile *tiles,
+                                    int32_t *n_tiles, int32_t tile_rows, uint8_t *xq, uint8_t *xs,
+                                    hipStream_t s);
 // Grouped products over stacked MXFP4 experts (expert e's rows at e * n of the
 // [E * n, k] cache).  mode 0 (up): rows gathered as perm[row] / topk; writes the codes
 // and scale bytes of fp32(relu(u)^2) to hq and hs, in bucket order.  mode 1 (down):
@@ -36,6 +43,14 @@ hipError_t launch_moe_mxfp4(int mode, int tile_rows, const uint8_t *aq, const ui
                             const uint8_t *wq, const uint8_t *ws, int64_t n, const MoETile *tiles,
                             const int32_t *n_tiles, int64_t max_tiles, float *out, uint8_t *hq,
                             uint8_t *hs, hipStream_t s);
+// The MoE layer of a few tokens in two launches, without bucketing (hq, hs: t * topk
+// hidden rows, in pair order).
+bool mxfp4_moe_direct_fits(int64_t t, int32_t topk);
+hipError_t launch_moe_mxfp4_direct(const uint16_t *x, int64_t t, int64_t k, const int32_t *ids,
+                                   const float *gates, int32_t topk, int32_t n_experts,
+                                   const uint8_t *w1, const uint8_t *s1, int64_t n1,
+                                   const uint8_t *w2, const uint8_t *s2, uint8_t *hq, uint8_t *hs,
+                                   float *out, hipStream_t s);
 
 // The router's training step.
 struct BalanceArgs {
@@ -45,8 +60,8 @@ struct BalanceArgs {
   int32_t n_experts, topk;
   int32_t sigmoid;
 };
-// Workgroups of the first launch; the scratch holds 2 * n_experts + 1 words for each.
-int balance_groups(int64_t t);
+// Bytes of scratch that launch_moe_balance needs (0: none), 8-byte aligned.
+size_t balance_scratch(int64_t t, int32_t n_experts);
 hipError_t launch_moe_balance(const BalanceArgs &a, float *loss, int32_t *counts, int32_t *tokens,
                               float *mean_p, void *scratch, hipStream_t s);
 struct RouterGradArgs {
