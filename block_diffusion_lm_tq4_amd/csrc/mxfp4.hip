@@ -809,6 +809,13 @@ constexpr int kBufferFlags = 0x00020000;
 // buffer loads into S stages, S - 1 ahead, with exact load-count waits and one barrier
 // per stage.
 //
+// Loads issue between the products (SPREAD, and always with PP): eight waves that first put a
+// stage's 60 loads into the memory pipe stand in front of it instead (4096 x 8192 x 2688:
+// 192 x 256 tiles 54.4 -> 51.7 us, 256 x 256 56.6 -> 52.0).  Only the MoE's 256-row tiles, which
+// have one stage on its way, want it as early as can be (4096 tokens 333 us, spread 335; 1024
+// tokens 210 and 225).  PP: two waves per SIMD half a step apart, one reading while the
+// other multiplies.
+//
 // Scale bytes are fetched CH steps at a time, 16 bytes a lane: 4 bytes of every row for
 // every step are as many cache lines to look up as the codes themselves (1024 tokens of
 // 128 experts: 245 us with them, 211 without any).
@@ -821,7 +828,8 @@ constexpr int kBufferFlags = 0x00020000;
 // row / 4 = 0 .. 3 of 64-byte rows put the 16 lanes of every phase on all 64
 // banks (of 32-row products row / 2 % 8 and row / 4 % 4).  Rows past the tile's end read zeros (dense; the
 // buffer range ends there) or the tile's first row (MoE) and are not stored.
-template <int MODE, int T, int WM, int WN, int MS, int NS, int KB, int S, int CH, bool PP>
+template <int MODE, int T, int WM, int WN, int MS, int NS, int KB, int S, int CH, bool PP,
+          bool SPREAD>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
   constexpr int W = WM * WN;
   constexpr int TM = T * MS * WM;
@@ -968,16 +976,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
   // or zeros) but not multiplied
   const int halves = g.kp / kStep;
   const int steps = KB == 64 ? halves : (halves + 1) / 2;
-  auto issue = [&](int c, uint8_t *st) __attribute__((always_inline)) {
+  // load i of a stage
+  auto issue_one = [&](int c, uint8_t *st, int i) __attribute__((always_inline)) {
     const int k0 = (c < steps ? c : steps - 1) * KB;  // padding steps reload the last one
-#pragma unroll
-    for (int i = 0; i < kALoads; ++i)
+    if (i < kALoads)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (lds_void *)(st + a_piece(i) * 1024), 16,
+                                               a_voff[i], k0, 0, 0);
+    else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          a_rsrc, (lds_void *)(st + a_piece(i) * 1024), 16, a_voff[i], k0, 0, 0);
+          w_rsrc, (lds_void *)(st + kWBase + w_piece(i - kALoads) * 1024), 16,
+          w_voff[i - kALoads], k0, 0, 0);
+  };
+  auto issue = [&](int c, uint8_t *st) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < kWLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          w_rsrc, (lds_void *)(st + kWBase + w_piece(i) * 1024), 16, w_voff[i], k0, 0, 0);
+    for (int i = 0; i < kLoads; ++i) issue_one(c, st, i);
   };
   auto issue_chunk = [&](int q) __attribute__((always_inline)) {
     if (q * CH >= halves) return;
@@ -1024,7 +1036,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
                  ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, c, 4, 4, 0, ws, 0, as)
                  : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, c, 4, 4, 2, ws, 2, as);
   };
-  auto half = [&](const uint8_t *st, int h, int step) __attribute__((always_inline)) {
+  // the products of step h of a stage; `between` after every row sub-tile
+  auto half = [&](const uint8_t *st, int h, int step, auto between)
+      __attribute__((always_inline)) {
     intx4 wf[NS][kProducts];
     int ws[NS];
 #pragma unroll
@@ -1036,15 +1050,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
     }
 #pragma unroll
     for (int i = 0; i < MS; ++i) {
-      if (MODE != kDense && i >= live) break;
-      const int as = scale_at(a_scale + T * WM * i * kRowScales, step);
+      if (MODE == kDense || i < live) {
+        const int as = scale_at(a_scale + T * WM * i * kRowScales, step);
 #pragma unroll
-      for (int p = 0; p < kProducts; ++p) {
-        const intx4 af =
-            *reinterpret_cast<const intx4 *>(st + a_frag + T * WM * i * KB + slot_at(h, p));
+        for (int p = 0; p < kProducts; ++p) {
+          const intx4 af =
+              *reinterpret_cast<const intx4 *>(st + a_frag + T * WM * i * KB + slot_at(h, p));
 #pragma unroll
-        for (int j = 0; j < NS; ++j) acc[i][j] = product(wf[j][p], af, acc[i][j], ws[j], as, p);
+          for (int j = 0; j < NS; ++j) acc[i][j] = product(wf[j][p], af, acc[i][j], ws[j], as, p);
+        }
       }
+      between(i);
     }
   };
 
@@ -1064,6 +1080,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
     };
+    // in a step's read phase the loads of S - 2 steps behind it have been issued, and those of
+    // the next one have to be through
+    constexpr int kAheadPP = (S - 3) * kLoads;
+    constexpr int kWaitPP = 0x0F70 | (kAheadPP & 15) | ((kAheadPP >> 4) << 14);
+    static_assert(S >= 3, "a step is in flight behind the next one");
     __builtin_amdgcn_s_waitcnt(kWait);  // step 0
     phase_end();
     if (late) phase_end();
@@ -1088,19 +1109,25 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
                   *reinterpret_cast<const intx4 *>(st + a_frag + T * WM * i * KB + slot_at(0, p));
             as[i] = scale_at(a_scale + T * WM * i * kRowScales, c + s);
           }
-          issue(c + s + S - 1, smem + ((s + S - 1) % S) * kStage);
-          if ((c + s) % kChunkStages == 0) issue_chunk((c + s) / kChunkStages + 1);
-          __builtin_amdgcn_s_waitcnt(kWait);   // step c + s + 1
-          __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+          __builtin_amdgcn_s_waitcnt(kWaitPP);  // step c + s + 1
+          __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
           phase_end();
+          // the stage read in the phase before last is refilled, a load at a time between the
+          // products
+          if ((c + s) % kChunkStages == 0) issue_chunk((c + s) / kChunkStages + 1);
 #pragma unroll
           for (int i = 0; i < MS; ++i) {
-            if (MODE != kDense && i >= live) break;
+            if (MODE == kDense || i < live) {
 #pragma unroll
-            for (int p = 0; p < kProducts; ++p)
+              for (int p = 0; p < kProducts; ++p)
 #pragma unroll
-              for (int j = 0; j < NS; ++j)
-                acc[i][j] = product(wf[j][p], af[i][p], acc[i][j], ws[j], as[i], p);
+                for (int j = 0; j < NS; ++j)
+                  acc[i][j] = product(wf[j][p], af[i][p], acc[i][j], ws[j], as[i], p);
+            }
+#pragma unroll
+            for (int l = i * kLoads / MS; l < (i + 1) * kLoads / MS; ++l)
+              issue_one(c + s + S - 1, smem + ((s + S - 1) % S) * kStage, l);
+            __builtin_amdgcn_sched_barrier(0);
           }
           phase_end();
         }
@@ -1117,13 +1144,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
         __builtin_amdgcn_s_waitcnt(kWait);
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
-        issue(c + s + S - 1, smem + ((s + S - 1) % S) * kStage);
+        if (c + s >= steps) break;
         if ((c + s) % kChunkStages == 0) issue_chunk((c + s) / kChunkStages + 1);
-        if (c + s < steps) {
-          half(smem + s * kStage, 0, kStageSteps * (c + s));
-          if (KB == 128 && 2 * (c + s) + 1 < halves)
-            half(smem + s * kStage, 1, kStageSteps * (c + s) + 1);
+        uint8_t *to = smem + ((s + S - 1) % S) * kStage;
+        if constexpr (SPREAD) {
+          auto between = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+            for (int l = i * kLoads / MS; l < (i + 1) * kLoads / MS; ++l)
+              issue_one(c + s + S - 1, to, l);
+            if (MS > 1) __builtin_amdgcn_sched_barrier(0);
+          };
+          half(smem + s * kStage, 0, kStageSteps * (c + s), between);
+        } else {
+          issue(c + s + S - 1, to);
+          half(smem + s * kStage, 0, kStageSteps * (c + s), [](int) {});
         }
+        if (KB == 128 && 2 * (c + s) + 1 < halves)
+          half(smem + s * kStage, 1, kStageSteps * (c + s) + 1, [](int) {});
       }
     }
   }
@@ -1153,7 +1190,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
   }
 }
 
-template <int MODE, int T, int WM, int WN, int MS, int NS, int KB, int S, int CH = 8, bool PP = false>
+template <int MODE, int T, int WM, int WN, int MS, int NS, int KB, int S, int CH = 8, bool PP = false,
+          bool SPREAD = true>
 hipError_t launch_tile(Fp4Args g, int64_t max_tiles, hipStream_t s) {
   constexpr int TM = T * MS * WM, TN = T * NS * WN;
   const int64_t n = MODE == kUp ? g.n_store : g.n;
@@ -1166,7 +1204,7 @@ hipError_t launch_tile(Fp4Args g, int64_t max_tiles, hipStream_t s) {
     grid = (max_tiles + 7) / 8 * 8 * g.tiles_n;
   }
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((fp4_tile_kernel<MODE, T, WM, WN, MS, NS, KB, S, CH, PP>),
+  hipLaunchKernelGGL((fp4_tile_kernel<MODE, T, WM, WN, MS, NS, KB, S, CH, PP, SPREAD>),
                      dim3(static_cast<unsigned>(grid)), dim3(64 * WM * WN), 0, s, g);
   return hipGetLastError();
 }
@@ -1174,23 +1212,23 @@ hipError_t launch_tile(Fp4Args g, int64_t max_tiles, hipStream_t s) {
 // The dense tile: the one with the least time, from the number of tiles and what each
 // kernel was measured to need (us): `alone` a step of 128 k with one workgroup on a compute
 // unit, `each` what every one adds where there are several, `slots` how many fit, `end`
-// a tile's start and stores; 256 compute units.  Fitted to sweeps over m = 17 .. 4096 at
-// (k, n) = (2688, 8192), (8192, 2688) and (1856, 2688), to which the three small tiles'
-// times are within 4 % and the large ones' within 7 to 19 %; the tile that it gives was the
-// fastest one, or within 1 %, at all of them.  (Times of the neighbours: 333 x 1856 x 2688 in
-// 32 x 64 tiles 6.8 us, 64 x 64 6.3, 64 x 128 8.6; 512 x 2688 x 8192 in 64 x 64 17.5,
-// 128 x 128 13.6, 192 x 256 20.3; 4096 x 2688 x 8192 in 128 x 128 75.6, 192 x 256 73.9,
-// 256 x 256 67.6; 4096 x 8192 x 2688 64.1, 55.6, 56.6.)
+// a tile's start and stores; 256 compute units.  Fitted to sweeps over m = 64 .. 4096 at
+// (k, n) = (2688, 8192), (8192, 2688) and (1856, 2688), to which the times of the tiles up to
+// 128 x 128 are within 5 % and the largest two's within 18 %; the tile that it gives was
+// the fastest one at all of them.  (Times of the neighbours: 333 x 1856 x 2688 in 32 x 64
+// tiles 6.8 us, 64 x 64 6.1, 64 x 128 8.8; 512 x 2688 x 8192 in 64 x 64 16.9, 128 x 128 13.2,
+// 192 x 256 18.6; 4096 x 2688 x 8192 in 128 x 128 70.4, 192 x 256 67.3, 256 x 256 63.6;
+// 4096 x 8192 x 2688 61.9, 51.7, 52.7.)
 int pick_tile(int64_t m, int64_t k, int64_t n) {
   struct Cost {
     int tm, tn, slots;
     double alone, each, end;
   };
   static constexpr Cost kCosts[] = {
-      {32, 32, 3, 0.107, 0.0445, 0.92},  {32, 64, 3, 0.103, 0.0698, 1.14},
-      {64, 64, 3, 0.151, 0.103, 1.46},   {64, 128, 2, 0.236, 0.132, 3.02},
-      {128, 128, 2, 0.10, 0.286, 2.97},  {192, 256, 1, 0.587, 0.587, 6.13},
-      {256, 256, 1, 0.574, 0.574, 8.77},
+      {32, 32, 3, 0.109, 0.0475, 0.56},  {32, 64, 3, 0.106, 0.0724, 0.98},
+      {64, 64, 3, 0.144, 0.0995, 1.35},  {64, 128, 2, 0.269, 0.148, 2.22},
+      {128, 128, 2, 0.295, 0.252, 3.00}, {192, 256, 1, 0.484, 0.484, 8.04},
+      {256, 256, 1, 0.481, 0.481, 11.7},
   };
   const double steps = static_cast<double>(mxfp4_padded_k(k) / kStep);
   int best = 0;
@@ -1434,8 +1472,9 @@ hipError_t launch_moe_mxfp4(int mode, int tile_rows, const uint8_t *aq, const ui
       if (mode == 0) return launch_tile<kUp, 32, 2, 4, 2, 1, 128, 2>(g, max_tiles, s);
       return launch_tile<kDown, 32, 2, 4, 2, 1, 128, 2>(g, max_tiles, s);
     case 256:
-      if (mode == 0) return launch_tile<kUp, 32, 2, 4, 4, 2, 128, 2>(g, max_tiles, s);
-      return launch_tile<kDown, 32, 2, 4, 4, 2, 128, 2>(g, max_tiles, s);
+      if (mode == 0)
+        return launch_tile<kUp, 32, 2, 4, 4, 2, 128, 2, 8, false, false>(g, max_tiles, s);
+      return launch_tile<kDown, 32, 2, 4, 4, 2, 128, 2, 8, false, false>(g, max_tiles, s);
     default: return hipErrorInvalidValue;
   }
 }
