@@ -31,6 +31,9 @@ def _require(cond: bool, msg: str) -> None:
 
 
 def _cuda_contig(t: torch.Tensor, name: str, dtype) -> None:
+    # (the messages below are built whether or not they are needed: 1.5 us a call)
+    if t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return
     _require(t.is_cuda, f"{name} must be a device tensor")
     _require(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
     _require(t.is_contiguous(), f"{name} must be contiguous")
