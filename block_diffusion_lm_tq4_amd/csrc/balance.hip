@@ -171,14 +171,19 @@ struct BalanceParts {
   uint32_t *done;  // slices that are through (cleared by the sums' launch)
 };
 
-// Sums over a workgroup, in wave order; every thread calls, thread 0 has the results.
-__device__ inline void group_sums(double &d, int64_t &n, double *lds_d, int64_t *lds_n) {
-  const int tid = threadIdx.x;
+// Sums over a wave; every lane has the results, and the same bits.
+__device__ inline void wave_sums(double &d, int64_t &n) {
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) {
     d += __shfl_xor(d, x);
     n += __shfl_xor(n, x);
   }
+}
+
+// Sums over a workgroup, in wave order; every thread calls, thread 0 has the results.
+__device__ inline void group_sums(double &d, int64_t &n, double *lds_d, int64_t *lds_n) {
+  const int tid = threadIdx.x;
+  wave_sums(d, n);
   if (tid % 64 == 0) {
     lds_d[tid / 64] = d;
     lds_n[tid / 64] = n;
@@ -299,7 +304,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a
 
 // A workgroup adds the groups' sums of its slice in a fixed order, fp64: thread e + 16 i
 // takes groups i, i + 64, ... of expert e, all on their way at once.  The last workgroup
-// through adds the slices' shares of the loss, in order.
+// through adds the slices' shares of the loss, a lane each, in a fixed order.
 __global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts parts, int groups,
                                                                    int n_experts, BalanceOut o) {
   constexpr int kParts = kSumThreads / kSlice;
@@ -308,8 +313,6 @@ __global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts 
   __shared__ double sp[kWaves][kSlice];
   __shared__ int32_t sc[kWaves][kSlice];
   __shared__ int32_t st;
-  __shared__ double dot[kSumThreads / 64];
-  __shared__ int64_t all[kSumThreads / 64];
   const int tid = threadIdx.x;
   const int col = tid % kSlice, part = tid / kSlice;
   const int e = static_cast<int>(blockIdx.x) * kSlice + col;
@@ -346,6 +349,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts 
   __syncthreads();
   if (t != 0) atomicAdd(&st, t);
   __syncthreads();
+  if (tid >= 64) return;  // lanes 0 .. 15 of wave 0 have the slice's experts
   double d = 0.0;
   int64_t n = 0;
   if (part == 0 && e < n_experts) {
@@ -356,25 +360,24 @@ __global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts 
     }
     balance_expert(o, e, p, c, st, d, n);
   }
-  group_sums(d, n, dot, all);
-  if (tid != 0) return;
-  if (blockIdx.x == 0) *o.tokens = st;
-  if (gridDim.x == 1) {
-    *o.loss = balance_loss(n_experts, d, n);
-    return;
+  wave_sums(d, n);
+  if (tid == 0 && blockIdx.x == 0) *o.tokens = st;
+  if (gridDim.x > 1) {
+    uint32_t before = 0;
+    if (tid == 0) {
+      parts.dot[blockIdx.x] = d;
+      parts.pairs[blockIdx.x] = n;
+      __threadfence();
+      before = atomicAdd(parts.done, 1u);
+    }
+    if (__builtin_amdgcn_readfirstlane(before) + 1 < gridDim.x) return;
+    __threadfence();
+    const bool in = tid < static_cast<int>(gridDim.x);  // at most 32 slices
+    d = in ? __hip_atomic_load(parts.dot + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+    n = in ? __hip_atomic_load(parts.pairs + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+    wave_sums(d, n);
   }
-  parts.dot[blockIdx.x] = d;
-  parts.pairs[blockIdx.x] = n;
-  __threadfence();
-  if (atomicAdd(parts.done, 1u) + 1 < gridDim.x) return;
-  __threadfence();
-  d = 0.0;
-  n = 0;
-  for (unsigned i = 0; i < gridDim.x; ++i) {
-    d += __hip_atomic_load(parts.dot + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    n += __hip_atomic_load(parts.pairs + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  *o.loss = balance_loss(n_experts, d, n);
+  if (tid == 0) *o.loss = balance_loss(n_experts, d, n);
 }
 
 // ---- gradient ------------------------------------------------------------------
