@@ -1195,11 +1195,11 @@ int tq4_moe_grouped_mxfp4(const uint16_t *x_bf16, int64_t t, int64_t k, const in
       tq4::launch_moe_mxfp4_prepare(x_bf16, t, k, topk_ids, topk, n_experts, counts, offsets, perm,
                                     inv, tiles, meta, l.tile_rows, xq, xs, s);
   if (e == hipSuccess)
-    e = tq4::launch_moe_mxfp4(0, l.tile_rows, xq, xs, t, k, perm, topk, w1_cache, w1_scales, n1,
-                              tiles, meta, l.max_tiles, nullptr, hq, hs, s);
+    e = tq4::launch_moe_mxfp4(0, l.tile_rows, xq, xs, t, k, perm, topk, n_experts, w1_cache,
+                              w1_scales, n1, tiles, meta, l.max_tiles, nullptr, hq, hs, s);
   if (e == hipSuccess)
-    e = tq4::launch_moe_mxfp4(1, l.tile_rows, hq, hs, pairs, n1, perm, topk, w2_cache, w2_scales,
-                              k, tiles, meta, l.max_tiles, o, nullptr, nullptr, s);
+    e = tq4::launch_moe_mxfp4(1, l.tile_rows, hq, hs, pairs, n1, perm, topk, n_experts, w2_cache,
+                              w2_scales, k, tiles, meta, l.max_tiles, o, nullptr, nullptr, s);
   if (e == hipSuccess) e = tq4::launch_combine(o, inv, topk_w, t, topk, k, out, s);
   return device_status(e);
 }
@@ -1257,6 +1257,10 @@ int tq4_moe_router_backward(const float *logits, int64_t t, int32_t n_experts,
   const uint64_t bytes = static_cast<uint64_t>(t) * n_experts * 4;
   if (overlap(dlogits, bytes, logits, bytes) || overlap(dlogits, bytes, topk_ids, pairs * 4) ||
       (dgates != nullptr && overlap(dlogits, bytes, dgates, pairs * 4)))
+    return TQ4_E_SHAPE;
+  // every workgroup reads these while others store
+  if (loss && (overlap(dlogits, bytes, counts, static_cast<uint64_t>(n_experts) * 4) ||
+               overlap(dlogits, bytes, tokens, 4) || overlap(dlogits, bytes, dloss, 4)))
     return TQ4_E_SHAPE;
   const tq4::RouterGradArgs a{{logits, topk_ids, t, n_experts, topk, score == TQ4_SCORE_SIGMOID},
                               dgates, renormalize, scale, counts, tokens, dloss, dlogits};

@@ -707,7 +707,7 @@ int tq4_moe_balance(const float *logits, int64_t t, int32_t n_experts, const int
  *            device; all three, or all NULL (no gradient from the loss)
  *   dlogits : [t, n_experts] fp32, device, overwritten; may not overlap an input
  * fp32, deterministic.  Errors: TQ4_E_SHAPE as tq4_moe_balance, and for a dlogits
- * that overlaps the logits, ids or dgates; TQ4_E_NULL (also for some but not all of
+ * that overlaps an input; TQ4_E_NULL (also for some but not all of
  * counts, tokens and dloss), TQ4_E_ALIGN (4-byte), TQ4_E_DEVICE.  t == 0 is a
  * no-op. */
 int tq4_moe_router_backward(const float *logits, int64_t t, int32_t n_experts,

@@ -37,7 +37,8 @@ def test_sizes(L):
     assert w(0, 2688, 8192) == w(100, 2690, 8192) == 0
     assert w(BIG, 64, 8) == w(100, 64, BIG) == 0 and w(1 << 24, 64, 8) > 0
     b = L.tq4_moe_balance_workspace_size
-    assert b(16, 128) >= 4 * 257 and b(0, 1) > 0
+    assert b(16, 128) == b(0, 1) == 0                               # one workgroup
+    assert b(1024, 128) >= 16 * 4 * 257
     assert b(-1, 128) == b(16, 0) == b(16, 513) == 0
 
 
@@ -157,10 +158,10 @@ def test_moe_errors(L):
 
 
 def test_balance_errors(L):
-    ws = L.tq4_moe_balance_workspace_size(40, 128)
+    ws = L.tq4_moe_balance_workspace_size(400, 128)   # (up to 256 tokens need none)
 
     def call(**kw):
-        a = dict(dict(l=FAKE, t=40, e=128, ids=FAKE, topk=6, score=0, loss=FAKE, c=FAKE, n=FAKE,
+        a = dict(dict(l=FAKE, t=400, e=128, ids=FAKE, topk=6, score=0, loss=FAKE, c=FAKE, n=FAKE,
                       p=FAKE, ws=FAKE, wsb=ws), **kw)
         return L.tq4_moe_balance(a["l"], a["t"], a["e"], a["ids"], a["topk"], a["score"],
                                  a["loss"], a["c"], a["n"], a["p"], a["ws"], a["wsb"], None)
@@ -192,7 +193,8 @@ def test_router_backward_errors(L):
         assert call(**{name: FAR + (1 << 26) + 2}) == E_ALIGN
     far = FAR + (1 << 28)
     for bad in (dict(l=FAR), dict(l=FAR + 40 * 512 - 4), dict(l=FAR - 40 * 512 + 4),
-                dict(ids=FAR + 400), dict(dg=FAR + 400), dict(ids=FAR - 40 * 24 + 4)):
+                dict(ids=FAR + 400), dict(dg=FAR + 400), dict(ids=FAR - 40 * 24 + 4),
+                dict(c=FAR + 400), dict(c=FAR - 512 + 4), dict(n=FAR), dict(dl=FAR + 400)):
         assert call(**dict(dict(l=far, ids=far, dg=far), **bad)) == E_SHAPE
     assert call(t=0, l=None, ids=None, out=None) == OK
 
