@@ -211,8 +211,8 @@ __device__ inline void balance_expert(const BalanceOut &o, int e, double p, int3
 }
 
 // A workgroup's share of the tokens.  With ONE workgroup its sums are the result, else its
-// sums of q and its counts go to scratch.  A token's row, and the ids, are fetched a round ahead where the
-// registers hold two rows.
+// sums of q and its counts go to scratch.  A token's row, and the ids, are fetched a round
+// ahead where the registers hold two rows.
 template <bool SIGMOID, int NV, bool VEC, bool ONE>
 __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a, BalanceOut o,
                                                                    BalanceParts parts) {

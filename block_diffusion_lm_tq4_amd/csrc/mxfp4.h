@@ -40,9 +40,9 @@ hipError_t launch_moe_mxfp4_prepare(const uint16_t *x, int64_t t, int64_t k, con
 int mxfp4_moe_tile_rows(int64_t pairs, int32_t n_experts);
 hipError_t launch_moe_mxfp4(int mode, int tile_rows, const uint8_t *aq, const uint8_t *as,
                             int64_t a_rows, int64_t k, const int32_t *perm, int32_t topk,
-                            const uint8_t *wq, const uint8_t *ws, int64_t n, const MoETile *tiles,
-                            const int32_t *n_tiles, int64_t max_tiles, float *out, uint8_t *hq,
-                            uint8_t *hs, hipStream_t s);
+                            int32_t n_experts, const uint8_t *wq, const uint8_t *ws, int64_t n,
+                            const MoETile *tiles, const int32_t *n_tiles, int64_t max_tiles,
+                            float *out, uint8_t *hq, uint8_t *hs, hipStream_t s);
 // The MoE layer of a few tokens in two launches, without bucketing (hq, hs: t * topk
 // hidden rows, in pair order).
 bool mxfp4_moe_direct_fits(int64_t t, int32_t topk);

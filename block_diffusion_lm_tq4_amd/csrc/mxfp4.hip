@@ -165,21 +165,22 @@ __global__ __launch_bounds__(kQThreads) void mxfp4_values_kernel(
     const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows,
     int64_t k, int64_t kp, uint16_t *__restrict__ out) {
   for (int64_t row = blockIdx.y; row < rows; row += gridDim.y)
-  for (int64_t at = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; at < k / 8;
-       at += static_cast<int64_t>(gridDim.x) * kQThreads) {
-    const uint32_t c = reinterpret_cast<const uint32_t *>(codes + row * (kp / 2))[at];
-    const uint32_t byte = scales[row * (kp / 32) + at / 4];
-    const float scale = scale_operand(byte);
-    const bool nan = byte == kNanScale;
-    uint32_t w[4];
-    w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0));
-    w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1));
-    w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2));
-    w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; at < k / 8;
+         at += static_cast<int64_t>(gridDim.x) * kQThreads) {
+      const uint32_t c = reinterpret_cast<const uint32_t *>(codes + row * (kp / 2))[at];
+      const uint32_t byte = scales[row * (kp / 32) + at / 4];
+      const float s = scale_operand(byte);
+      bf16x2 v[4];
+      v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0);
+      v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1);
+      v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2);
+      v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3);
+      uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = nan ? 0x7FC07FC0u : w[i];
-    reinterpret_cast<uint4 *>(out + row * k)[at] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+      for (int i = 0; i < 4; ++i)
+        w[i] = byte == kNanScale ? 0x7FC07FC0u : __builtin_bit_cast(uint32_t, v[i]);
+      reinterpret_cast<uint4 *>(out + row * k)[at] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 // Packed TQ4_1S rows: one thread per block, decoded (rotation undone) and encoded in
@@ -289,7 +290,8 @@ __device__ inline uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((pair{a, b}), bf16x2));
 }
 
-// A wave's 16 x 16 block of a dense output: row lane % 16 of `rows` valid ones, columns n0 + 4 (lane / 16) ....
+// A wave's 16 x 16 block of a dense output: row lane % 16 of `rows` valid ones, columns n0 +
+// 4 (lane / 16) .. + 3.
 template <bool BF16, bool VEC>
 __device__ inline void store_block(const Fp4Args &g, floatx4 acc, int rows, int64_t n0, int lane) {
 #pragma clang fp contract(off)
@@ -811,10 +813,9 @@ constexpr int kBufferFlags = 0x00020000;
 //
 // Loads issue between the products (SPREAD, and always with PP): eight waves that first put a
 // stage's 60 loads into the memory pipe stand in front of it instead (4096 x 8192 x 2688:
-// 192 x 256 tiles 54.4 -> 51.7 us, 256 x 256 56.6 -> 52.0).  Only the MoE's 256-row tiles, which
-// have one stage on its way, want it as early as can be (4096 tokens 333 us, spread 335; 1024
-// tokens 210 and 225).  PP: two waves per SIMD half a step apart, one reading while the
-// other multiplies.
+// 192 x 256 tiles 54.4 -> 51.7 us, 256 x 256 56.6 -> 52.0).  Only the MoE's 256-row tiles where
+// every expert's weights are read once, with one stage on its way, want it as early as can
+// be.  PP: two waves per SIMD half a step apart, one reading while the other multiplies.
 //
 // Scale bytes are fetched CH steps at a time, 16 bytes a lane: 4 bytes of every row for
 // every step are as many cache lines to look up as the codes themselves (1024 tokens of
@@ -826,8 +827,8 @@ constexpr int kBufferFlags = 0x00020000;
 // of lane r + 16 g reading row r, a phase holds rows 0-3 and 12-15 at one slot
 // and 4-11 at another.  key = (row / 2) % 8 for 128-byte rows and 0, 2, 3, 1 for
 // row / 4 = 0 .. 3 of 64-byte rows put the 16 lanes of every phase on all 64
-// banks (of 32-row products row / 2 % 8 and row / 4 % 4).  Rows past the tile's end read zeros (dense; the
-// buffer range ends there) or the tile's first row (MoE) and are not stored.
+// banks (T = 32: (row / 2) % 8 and (row / 4) % 4).  Rows past the tile's end read zeros
+// (dense; the buffer range ends there) or the tile's first row (MoE) and are not stored.
 template <int MODE, int T, int WM, int WN, int MS, int NS, int KB, int S, int CH, bool PP,
           bool SPREAD>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
@@ -937,7 +938,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
     const int p = kWLoads * wave + i;
     return p < kWPieces ? p : kWPieces - 1;
   };
-  uint32_t a_voff[8];  // (a bound that depends on the template made the host pass drop launch stubs)
+  // (a bound that depends on the template made the host pass drop launch stubs)
+  uint32_t a_voff[8];
 #pragma unroll
   for (int i = 0; i < kALoads; ++i) {
     const int row = kPieceRows * a_piece(i) + prow;
@@ -1190,8 +1192,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
   }
 }
 
-template <int MODE, int T, int WM, int WN, int MS, int NS, int KB, int S, int CH = 8, bool PP = false,
-          bool SPREAD = true>
+template <int MODE, int T, int WM, int WN, int MS, int NS, int KB, int S, int CH = 8,
+          bool PP = false, bool SPREAD = true>
 hipError_t launch_tile(Fp4Args g, int64_t max_tiles, hipStream_t s) {
   constexpr int TM = T * MS * WM, TN = T * NS * WN;
   const int64_t n = MODE == kUp ? g.n_store : g.n;
@@ -1442,9 +1444,9 @@ hipError_t launch_moe_mxfp4_direct(const uint16_t *x, int64_t t, int64_t k, cons
 
 hipError_t launch_moe_mxfp4(int mode, int tile_rows, const uint8_t *aq, const uint8_t *as,
                             int64_t a_rows, int64_t k, const int32_t *perm, int32_t topk,
-                            const uint8_t *wq, const uint8_t *ws, int64_t n, const MoETile *tiles,
-                            const int32_t *n_tiles, int64_t max_tiles, float *out, uint8_t *hq,
-                            uint8_t *hs, hipStream_t s) {
+                            int32_t n_experts, const uint8_t *wq, const uint8_t *ws, int64_t n,
+                            const MoETile *tiles, const int32_t *n_tiles, int64_t max_tiles,
+                            float *out, uint8_t *hq, uint8_t *hs, hipStream_t s) {
   if (max_tiles > 65535 || n % 32 != 0) return hipErrorInvalidValue;
   if (max_tiles == 0) return hipSuccess;
   Fp4Args g{};
@@ -1471,10 +1473,18 @@ hipError_t launch_moe_mxfp4(int mode, int tile_rows, const uint8_t *aq, const ui
     case 128:
       if (mode == 0) return launch_tile<kUp, 32, 2, 4, 2, 1, 128, 2>(g, max_tiles, s);
       return launch_tile<kDown, 32, 2, 4, 2, 1, 128, 2>(g, max_tiles, s);
-    case 256:
+    case 256: {
+      // With several tiles to an expert the loads go between the products (see the kernel):
+      // 8192 tokens of 128 experts 622 -> 606 us, 3000 of 8 230 -> 220, but 4096 of 128
+      // (192 rows an expert) 329 -> 334 and 2048 252 -> 265.
+      const int64_t pairs = mode == 0 ? a_rows * topk : a_rows;
+      const bool spread = pairs > 240 * static_cast<int64_t>(n_experts);
       if (mode == 0)
-        return launch_tile<kUp, 32, 2, 4, 4, 2, 128, 2, 8, false, false>(g, max_tiles, s);
-      return launch_tile<kDown, 32, 2, 4, 4, 2, 128, 2, 8, false, false>(g, max_tiles, s);
+        return spread ? launch_tile<kUp, 32, 2, 4, 4, 2, 128, 2>(g, max_tiles, s)
+                      : launch_tile<kUp, 32, 2, 4, 4, 2, 128, 2, 8, false, false>(g, max_tiles, s);
+      return spread ? launch_tile<kDown, 32, 2, 4, 4, 2, 128, 2>(g, max_tiles, s)
+                    : launch_tile<kDown, 32, 2, 4, 4, 2, 128, 2, 8, false, false>(g, max_tiles, s);
+    }
     default: return hipErrorInvalidValue;
   }
 }

@@ -86,11 +86,12 @@ def _experts(dev, e, n, k, seed):
             [(c[i * n:(i + 1) * n], s[i * n:(i + 1) * n]) for i in range(e)])
 
 
-# few pairs (the single-token form, up to 24), then 64-, 128- and 256-row tiles
+# few pairs (the single-token form, up to 24), then 64-, 128- and 256-row tiles, the last with
+# one tile and with several to an expert
 MOE = [(1, 4, 1, 2080, 1184), (3, 16, 8, 96, 352), (4, 8, 6, 1152, 640), (24, 30, 1, 160, 96),
        (2, 12, 9, 128, 64), (60, 12, 4, 2080, 1184), (25, 64, 1, 352, 2080),
        (100, 8, 5, 2080, 1184), (120, 8, 4, 160, 2080), (300, 6, 4, 2080, 1184),
-       (513, 2, 1, 96, 1152)]
+       (513, 2, 1, 96, 1152), (700, 4, 2, 2080, 1184)]
 
 
 @pytest.mark.parametrize("t,e,topk,k,n1", MOE)
