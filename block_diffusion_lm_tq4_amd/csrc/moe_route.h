@@ -1,7 +1,7 @@
 // Device routines of the MoE routing shared by the routing kernels (moe.hip,
-// int8.hip, router.hip) and the persistent MoE block kernel (gemm.hip): the router for one token,
-// the stable bucketing of token-expert pairs by expert and the weighted
-// combine.  Nemotron-TheHobbit-30B-A3B model card: section The model
+// int8.hip, mxfp4.hip, router.hip) and the persistent MoE block kernel (gemm.hip): the
+// router for one token, the stable bucketing of token-expert pairs by expert and the
+// weighted combine.  Nemotron-TheHobbit-30B-A3B model card: section The model
 // underneath (128-expert MoE, top-6) and section Running it ("sync-free
 // MoE").  Included inside namespace tq4's anonymous namespace.
 #pragma once

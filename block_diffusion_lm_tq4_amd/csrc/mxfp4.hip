@@ -15,13 +15,14 @@
 // Layout.  Two codes a byte, the first in the low half; rows padded with zero codes and
 // zero scale bytes to kp, k rounded up to a multiple of 128 (the k of one MFMA step).
 //
-// Products run on v_mfma_scale_f32_16x16x128_f8f6f4: lane i + 16 g holds the 32 values
-// k = 32 g .. 32 g + 31 of row i of each operand as they lie in memory (16 bytes), and
-// their scale byte.  A product of two codes is a multiple of 0.25 up to 36, so a block's
-// sum is exact, and a row's is while 2^24 times the smallest unit 0.25 * 2^(e + f) it
+// Products run on v_mfma_scale_f32_16x16x128_f8f6f4 and v_mfma_scale_f32_32x32x64_f8f6f4:
+// lane i + 16 g (i + 32 g) holds the 32 values k = 32 g .. 32 g + 31 of row i of each operand as
+// they lie in memory (16 bytes), and their scale byte.  In a pure loop on random codes they reach
+// 4.3 to 4.7 and 5.7 to 6.0 PF.  A product of two codes is a multiple of 0.25 up to 36, so a
+// block's sum is exact, and a row's is while 2^24 times the smallest unit 0.25 * 2^(e + f) it
 // meets holds it; below that every split of k gives the same bits, past it sums round to
-// fp32.  The weights are the first operand: lane i + 16 g of the result
-// holds columns n = 4 g .. 4 g + 3 of token i, four consecutive outputs.
+// fp32.  The weights are the first operand: a lane of the result holds outputs of one token, four
+// consecutive columns at a time.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -119,7 +120,8 @@ __device__ inline void act_pieces(const uint4 *xr, int64_t k, int64_t kp, int64_
   }
 }
 
-// Grid: pieces of a row x rows.  HBM-bound: 2.53 bytes per value.
+// Grid: pieces of a row x rows.  Bound by memory, 2.53 bytes per value (4096 x 8192 15.4 us,
+// 5.5 TB/s; what a copy reaches).  Two pieces per thread keep enough loads on their way.
 template <int V>
 __global__ __launch_bounds__(kQThreads) void act_mxfp4_kernel(const uint16_t *__restrict__ x,
                                                               int64_t rows, int64_t k, int64_t kp,
@@ -136,7 +138,8 @@ __global__ __launch_bounds__(kQThreads) void act_mxfp4_kernel(const uint16_t *__
 // The MoE layer's first launch: workgroup 0 buckets the pairs, the waves of the others
 // quantize the tokens, 128 pieces of a row each.  Neither needs the other's result, and
 // the bucketing is one workgroup's chain of latencies in which the rest of the device is
-// free.
+// free (16 tokens 6.4 us, 1024 11.2: the bucketing's own time), and a launch costs the host
+// 3.1 to 3.6 us.
 __global__ __launch_bounds__(kRouteThreads) void fp4_route_act_kernel(
     const int32_t *ids, int64_t pairs, int32_t n_experts, int32_t *counts, int32_t *offsets,
     int32_t *perm, int32_t *inv, MoETile *tiles, int32_t *n_tiles, int32_t tile_rows,
@@ -160,7 +163,8 @@ __global__ __launch_bounds__(kRouteThreads) void fp4_route_act_kernel(
 }
 
 // The values that codes stand for, as bf16 (exact: a code has one mantissa bit; what
-// the largest scales put past bf16's range is infinite).  A thread takes 8.
+// the largest scales put past bf16's range is infinite).  A thread takes 8.  Bound by
+// memory (4096 x 8192 14.4 us, 5.9 TB/s).
 __global__ __launch_bounds__(kQThreads) void mxfp4_values_kernel(
     const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows,
     int64_t k, int64_t kp, uint16_t *__restrict__ out) {
@@ -493,8 +497,10 @@ __device__ inline void stream(const uint8_t *const (&wq)[NT], const uint8_t *con
 }
 
 // bf16 rows against 16 NT columns per workgroup of KW waves, which share k.  Their sums meet
-// in LDS and are added in wave order.  Dense: up to 16 rows.  Up: a workgroup row per pair,
-// the expert from the ids, hidden rows in pair order.
+// in LDS and are added in wave order.  Every workgroup quantizes the rows for itself: a
+// launch of its own would cost the host more (one row of 2688 x 8192 5.4 us, 2.2 TB/s of
+// weights: the ramp of a short stream; 16 rows 7.7, the row pieces 2.3 of them).  Dense: up to
+// 16 rows.  Up: a workgroup row per pair, the expert from the ids, hidden rows in pair order.
 template <int MODE, int NT, int KW, int B>
 __global__ __launch_bounds__(64 * KW) void fp4_skinny_kernel(Fp4Args g) {
   static_assert(MODE == kDense || (MODE == kUp && NT == 2), "a hidden block is two sub-tiles");
@@ -563,7 +569,8 @@ __global__ __launch_bounds__(64 * KW) void fp4_skinny_kernel(Fp4Args g) {
 
 // The down product of few tokens with the weighted sum over their slots: grid (blocks of 16
 // columns, tokens); waves KW j .. KW j + KW - 1 share the k of slot j.  Hidden rows are in pair
-// order.  The sum runs in slot order with the combine kernel's fused multiply-adds.
+// order.  The sum runs in slot order with the combine kernel's fused multiply-adds.  One
+// token of six slots, 1856 x 2688: 6.2 us (2.7 TB/s), the ramp of a 16 MB stream.
 constexpr int kDirectSlots = 8;
 
 template <int KW, int B>
@@ -820,6 +827,13 @@ constexpr int kBufferFlags = 0x00020000;
 // Scale bytes are fetched CH steps at a time, 16 bytes a lane: 4 bytes of every row for
 // every step are as many cache lines to look up as the codes themselves (1024 tokens of
 // 128 experts: 245 us with them, 211 without any).
+//
+// 4096 x 8192 x 2688 in 192 x 256 tiles: 52 us, 3.5 PF; matrix units busy in 48 % of the
+// cycles, the rest loads into LDS; weights straight to registers took 79 to 101.  MoE layer of
+// 128 experts of 1856 x 2688: 16 tokens 46 us up and 39 down (4.4 and 5.3 TB/s of weights),
+// 1024 tokens 96 and 101 (4.8 and 5.2 TB/s with rows that two XCDs read), 4096 tokens 118 and 146
+// (3.8 and 4.7 TB/s with what they write): bound by memory, the up product of 4096 tokens by the
+// one stage on its way, and deeper forms of fewer columns read more and took longer.
 //
 // LDS image of a stage: 1 KB pieces of 1024 / KB rows; a row's 16-byte slots
 // are stored at slot ^ key(row).  A 16-byte read takes the wave in phases of 16
