@@ -279,7 +279,7 @@ struct Fp4Args {
   const int32_t *perm; // MoE: bucket order (up gathers through it)
   const MoETile *tiles;
   const int32_t *n_tiles;
-  int32_t tile_run;    // consecutive tiles that an XCD takes
+  int32_t tile_run;    // consecutive tiles that an XCD takes (tiles of more than 64 rows)
   int64_t a_rows;      // MoE: rows of xq
   int32_t topk;
   const int32_t *ids;  // MoE of few pairs: [t][topk], and
@@ -904,15 +904,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
     n_base = static_cast<int64_t>(8 * blk + in % width) * TN;
     rows = g.m - m_base < TM ? static_cast<int>(g.m - m_base) : TM;
   } else {
-    // XCD x (workgroup id % 8) takes runs of g.tile_run tiles, x, x + 8, ..., a tile's
-    // column blocks in a row: the tile's rows then stay in one L2
-    const int q = static_cast<int>(blockIdx.x) / 8;
-    const int s = q / g.tiles_n;
-    const int i = (s / g.tile_run * 8 + static_cast<int>(blockIdx.x) % 8) * g.tile_run +
-                  s % g.tile_run;
+    int i, j;
+    if constexpr (TM <= 64) {
+      // Tiles of few rows: their column blocks in a row, over all XCDs.  The rows that every
+      // XCD then reads are small beside the weights, and no XCD gets a tile more than
+      // another (16 tokens 97 us with whole tiles to an XCD, 87 so; 128-row tiles 201 and
+      // 202, 256-row 339 and 347).
+      i = static_cast<int>(blockIdx.x) / g.tiles_n;
+      j = static_cast<int>(blockIdx.x) % g.tiles_n;
+    } else {
+      // XCD x (workgroup id % 8) takes runs of g.tile_run tiles, x, x + 8, ..., a tile's
+      // column blocks in a row: the tile's rows then stay in one L2
+      const int q = static_cast<int>(blockIdx.x) / 8;
+      const int s = q / g.tiles_n;
+      i = (s / g.tile_run * 8 + static_cast<int>(blockIdx.x) % 8) * g.tile_run + s % g.tile_run;
+      j = q % g.tiles_n;
+    }
     if (i >= *g.n_tiles) return;
     const MoETile t = g.tiles[i];
-    const int j = q % g.tiles_n;
     m_base = t.row0;
     rows = t.rows;
     n_base = static_cast<int64_t>(j) * TN;
