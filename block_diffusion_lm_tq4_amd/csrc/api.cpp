@@ -1118,7 +1118,7 @@ struct MoEFp4Layout {
 MoEFp4Layout moe_fp4_layout(int64_t t, int32_t topk, int32_t e, int64_t n1, int64_t k) {
   const int64_t pairs = t * topk;
   MoEFp4Layout l{};
-  l.tile_rows = tq4::mxfp4_moe_tile_rows(pairs, e);
+  l.tile_rows = tq4::mxfp4_moe_tile_rows(pairs, e, n1, k);
   const int64_t busy = pairs < e ? pairs : e;
   l.max_tiles = pairs / l.tile_rows + busy + 1;
   const size_t p = static_cast<size_t>(pairs);

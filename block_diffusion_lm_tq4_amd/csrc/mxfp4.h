@@ -37,7 +37,7 @@ hipError_t launch_moe_mxfp4_prepare(const uint16_t *x, int64_t t, int64_t k, con
 // and scale bytes of fp32(relu(u)^2) to hq and hs, in bucket order.  mode 1 (down):
 // bucket rows; out is fp32 [pairs][n].  tile_rows as mxfp4_moe_tile_rows gives (and
 // launch_route got).
-int mxfp4_moe_tile_rows(int64_t pairs, int32_t n_experts);
+int mxfp4_moe_tile_rows(int64_t pairs, int32_t n_experts, int64_t n1, int64_t k);
 hipError_t launch_moe_mxfp4(int mode, int tile_rows, const uint8_t *aq, const uint8_t *as,
                             int64_t a_rows, int64_t k, const int32_t *perm, int32_t topk,
                             int32_t n_experts, const uint8_t *wq, const uint8_t *ws, int64_t n,

@@ -1417,10 +1417,22 @@ hipError_t launch_linear_mxfp4(const uint8_t *xq, const uint8_t *xs, int64_t m, 
 // 95 to 105; 1.5 rows 130 and 123; 12 rows 161 / 159, 32-row 158 / 170, 128-row 164 / 161; 48
 // rows 197 / 232, 128-row 202 / 219, 256-row 210 / 228; 96 rows 128-row 258 / 286, 256-row
 // 253 / 286; 192 rows 410 / 425 and 330 / 387.
-int mxfp4_moe_tile_rows(int64_t pairs, int32_t n_experts) {
+// A height is halved where its workgroups (256 or, up to 128 rows, 128 columns each) would leave
+// half of the compute units idle: 300 tokens of 8 experts, topk 6, 256-row tiles 57, 128-row 41
+// (500 tokens 55 and 61); 500 tokens of 2 experts, one slot, 128-row 34, 64-row 28 (2000 tokens
+// 45 and 52).
+int mxfp4_moe_tile_rows(int64_t pairs, int32_t n_experts, int64_t n1, int64_t k) {
   const int64_t e = n_experts;
-  if (pairs <= 36 * e) return 64;
-  return pairs <= 80 * e ? 128 : 256;
+  const int64_t busy = pairs < e ? pairs : e;
+  int rows = pairs <= 36 * e ? 64 : pairs <= 80 * e ? 128 : 256;
+  while (rows > 64) {
+    const int64_t tiles = busy * ((pairs + busy * rows - 1) / (busy * rows));
+    const int64_t cols = rows == 256 ? 256 : 128;
+    const int64_t blocks = (mxfp4_padded_k(n1) + cols - 1) / cols + (k + cols - 1) / cols;
+    if (tiles * blocks >= 256) break;  // of both products: 128 each
+    rows /= 2;
+  }
+  return rows;
 }
 
 // Up to 24 pairs (four tokens of six slots): one to four tokens 14.7, 22.0, 29.9 and 38.9 us,

@@ -87,11 +87,14 @@ def _experts(dev, e, n, k, seed):
 
 
 # few pairs (the single-token form, up to 24), then 64-, 128- and 256-row tiles, the last with
-# one tile and with several to an expert
+# one tile and with several to an expert; few workgroups have lower and narrower tiles
 MOE = [(1, 4, 1, 2080, 1184), (3, 16, 8, 96, 352), (4, 8, 6, 1152, 640), (24, 30, 1, 160, 96),
        (2, 12, 9, 128, 64), (60, 12, 4, 2080, 1184), (25, 64, 1, 352, 2080),
        (100, 8, 5, 2080, 1184), (120, 8, 4, 160, 2080), (300, 6, 4, 2080, 1184),
-       (513, 2, 1, 96, 1152), (700, 4, 2, 2080, 1184)]
+       (513, 2, 1, 96, 1152), (700, 4, 2, 2080, 1184),
+       (150, 10, 4, 2080, 1184), (600, 45, 4, 96, 1184),
+       (1000, 20, 4, 2080, 1184), (1150, 45, 4, 96, 1184),
+       (1250, 10, 4, 2080, 1184), (1280, 15, 6, 352, 2080)]
 
 
 @pytest.mark.parametrize("t,e,topk,k,n1", MOE)
