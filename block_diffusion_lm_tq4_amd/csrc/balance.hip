@@ -418,18 +418,27 @@ __device__ inline float gate_part(const RouterGradArgs &g, int64_t t, const Slot
     if (b > 0) s.load(g, t, b * kLanes + lane);
     return s;
   };
-  float base = top, norm = inv, mean = 0.f;
+  float base = top, norm = inv, mean = 0.f, ref = 0.f;
   if (g.renormalize) {  // scores relative to the largest chosen one
     base = kOff;
     for (int b = 0; b < blocks; ++b) base = __builtin_fmaxf(base, slot(b).l);
     base = row_max(base);
+    // dw_j - sum_i u_i dw_i is taken relative to the dw of the largest one: with one slot, or
+    // one that has nearly all the weight, the two sides of the difference are all but equal
+    ref = kOff;
+    for (int b = 0; b < blocks; ++b) {
+      const Slot s = slot(b);
+      if (s.l > kOff && s.l == base) ref = __builtin_fmaxf(ref, s.d);
+    }
+    ref = row_max(ref);
+    ref = ref > kOff ? ref : 0.f;
     float sum = 0.f, dot = 0.f;
     for (int b = 0; b < blocks; ++b) {
       const Slot s = slot(b);
       float rest;
       const float p = s.l > kOff ? score<SIGMOID>(s.l, base, rest) : 0.f;
       sum += p;
-      dot += p * s.d;
+      dot += p * (s.d - ref);
     }
     sum = row_sum(sum);
     norm = sum > 0.f ? 1.f / sum : 0.f;
@@ -444,7 +453,7 @@ __device__ inline float gate_part(const RouterGradArgs &g, int64_t t, const Slot
     const int id = s.id;
     float rest = 1.f;
     const float p = s.l > kOff ? score<SIGMOID>(s.l, base, rest) * norm : 0.f;
-    float add = p * (g.scale * (s.d - mean));
+    float add = p * (g.scale * ((s.d - ref) - mean));
     taken += add;
     if (SIGMOID) add *= rest;
     // Slots that all have experts of their own, as a router's have, add without a look at

@@ -93,6 +93,36 @@ def test_balance_of_a_million_tokens(dev, score):
     assert abs(float(loss) - ref) <= (150 + 68) * U * ref
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_of_weights_that_are_all_but_one(dev, score):
+    """A renormalized weight is constant where a token has one slot, and nearly where one of
+    its slots has nearly all of it: only what is left of the gradient may remain."""
+    o = _ops()
+    rng = np.random.default_rng(0)
+    t, e = 60, 16
+    l = rng.standard_normal((t, e)).astype(np.float32)
+    lg = torch.from_numpy(l).to(dev)
+    ids, _ = o.moe_router_scored(lg, 1, score=score, renormalize=True)
+    loss, counts, tokens, _ = o.moe_balance(lg, ids, score=score)
+    rest = dict(score=score, renormalize=True, scale=2.5, counts=counts, tokens=tokens, dloss=loss)
+    one = o.moe_router_backward(lg, ids, torch.randn(t, 1, device=dev), **rest)
+    assert torch.equal(one, o.moe_router_backward(lg, ids, torch.zeros(t, 1, device=dev), **rest))
+    l[:, 0] = -40 if score == "sigmoid" else 0
+    l[:, 1:] = l[:, :1] - 12 - np.arange(15, dtype=np.float32)
+    i = np.tile(np.array([[1, 0, 2]], np.int32), (t, 1))
+    d = rng.standard_normal((t, 3)).astype(np.float32)
+    grad = o.moe_router_backward(torch.from_numpy(l).to(dev), torch.from_numpy(i).to(dev),
+                                 torch.from_numpy(d).to(dev), score=score, renormalize=True)
+    p = np.exp(l[:, :3].astype(np.float64) - l[:, :1])     # (sigmoid of -40: 1 + e^l is 1)
+    u = p / p.sum(1, keepdims=True)
+    by = d[:, [1, 0, 2]].astype(np.float64)
+    diff = by[:, :, None] - by[:, None, :]                 # dw_j - dw_i
+    want = u * (diff * u[:, None, :]).sum(2)
+    size = u * (np.abs(diff) * u[:, None, :]).sum(2)
+    # differences of logits up to 14: (4 * 14 + 160) roundings, as test_gpu_balance.py counts
+    assert np.all(np.abs(grad[:, :3].double().cpu().numpy() - want) <= (4 * 14 + 160) * U * size)
+
+
 def test_graphs_that_share_a_workspace(dev):
     """Two graphs on one stream with the same scratch memory, replayed in turn."""
     o = _ops()
