@@ -3,7 +3,8 @@
 // wanted: a resident copy that no forward decodes) on 4-bit floating-point operands.
 //
 // Rows.  32 consecutive values of a row share a scale 2^e, held as the byte e + 127;
-// with a = max|v|, e is the smallest integer from -127 with a < 7 * 2^e.  A value is
+// with a = max|v|, e is the smallest integer from -127 to 127 with a < 7 * 2^e (127 where there
+// is none: byte 255 is no scale, and weights that packed rows decode to reach 2^132).  A value is
 // held as the e2m1 code (sign, two exponent bits, one mantissa bit: 0, 0.5, 1, 1.5,
 // 2, 3, 4, 6) nearest to v / 2^e, ties to the even code; what lies between 6 and 7 becomes
 // 6.  (Letting a up to 7 * 2^e in costs the largest values at most as much as
@@ -246,7 +247,7 @@ __global__ __launch_bounds__(kQThreads) void mxfp4_cache_kernel(
           int p2;
           const double f = __builtin_frexp(top, &p2);
           e = p2 - 3 + (f >= 0.875 ? 1 : 0);
-          e = e < -127 ? -127 : e;
+          e = e < -127 ? -127 : (e > 127 ? 127 : e);  // (codes of 6 where it stops)
         }
         byte = static_cast<uint32_t>(e + 127);
 #pragma unroll

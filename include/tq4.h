@@ -441,11 +441,13 @@ int tq4_moe_grouped_int8(const uint16_t *x_bf16, int64_t t, int64_t k, const int
  * forward decodes): 4.25 bits per weight, activations quantized per call.
  *
  * 32 consecutive k of a row share a scale 2^e stored as the E8M0 byte e + 127;
- * with a = max|v| of the block, e is the smallest integer from -127 with a <
- * 7 * 2^e.  A value is held as the OCP e2m1 code (bit 3 sign, bits 2-1
- * exponent, bit 0 mantissa: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) nearest to
- * v / 2^e, ties to the even code, 6 at most; the sign is kept, also of zero.  A
- * block holding a NaN or an infinity has scale byte 255 (NaN) and zero codes.
+ * with a = max|v| of the block, e is the smallest integer from -127 to 127 with a
+ * < 7 * 2^e, or 127 where there is none (bf16 values stay below 7 * 2^126; weights
+ * decoded from packed rows need not).  A value is held as the OCP e2m1 code (bit 3
+ * sign, bits 2-1 exponent, bit 0 mantissa: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6)
+ * nearest to v / 2^e, ties to the even code, 6 at most; the sign is kept, also of
+ * a bf16 zero.  A block holding a NaN or an infinity has scale byte 255 (NaN) and
+ * zero codes.
  * Two codes a byte, the lower k in the low half.  Rows are padded to kp = k
  * rounded up to a multiple of 128 with zero codes and zero scale bytes, which
  * add nothing to a product.  A cache of an [n, k] matrix is the codes
@@ -457,8 +459,9 @@ int tq4_moe_grouped_int8(const uint16_t *x_bf16, int64_t t, int64_t k, const int
 size_t tq4_mxfp4_cache_size(int64_t n, int64_t k);
 
 /* Build the cache from a packed [n][k/32][20] matrix (device, 4-byte
- * aligned): the decoded weights W_hat (rotation undone) held as above, the
- * decoding and the choices in fp64.  cache: device, 16-byte aligned,
+ * aligned): the decoded weights W_hat (rotation undone; their zeros without a
+ * sign) held as above, the decoding and the choices in fp64.  A block whose scales
+ * are not finite counts as one that holds a NaN.  cache: device, 16-byte aligned,
  * tq4_mxfp4_cache_size bytes.  Offline, like tq4_pack.  Errors: TQ4_E_NULL,
  * TQ4_E_SHAPE, TQ4_E_ALIGN, TQ4_E_DEVICE.  n == 0 or k == 0 is a no-op. */
 int tq4_mxfp4_cache(const uint8_t *packed, int64_t n, int64_t k, uint32_t sign_bits,

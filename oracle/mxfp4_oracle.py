@@ -8,9 +8,9 @@ every forward runs; *Help wanted*: a resident copy; *The model underneath*: 128
 experts, top-6):
 
 * 32 consecutive values of a row share a scale 2^e (byte e + 127), e the smallest
-  integer from -127 with max|v| < 7 * 2^e; a value is the e2m1 code nearest to
-  v / 2^e, ties to the even code, 6 at most; a block with a NaN or an infinity has
-  byte 255 and zero codes;
+  integer from -127 to 127 with max|v| < 7 * 2^e, or 127 where there is none; a value
+  is the e2m1 code nearest to v / 2^e, ties to the even code, 6 at most; a block with a
+  NaN or an infinity has byte 255 and zero codes;
 * weights: the decoded TQ4_1S weights or BF16 weights; activations: per call;
 * y[m, n] = the exact sum of the products of the values;
 * the MoE layer quantizes its hidden values fp32(fp32(relu(u))^2) the same way;
@@ -49,9 +49,10 @@ def mxfp4_rows(v: np.ndarray) -> tuple[np.ndarray, np.ndarray]:
             if not up.any():
                 break
             e = e + step * up
+    e = np.minimum(e, 127)                        # the largest scale: values past 6 * 2^127 become it
     u = np.ldexp(np.where(good[..., None], b, 0.0), -e[..., None])
-    a = np.abs(u)
-    hi = np.minimum(np.searchsorted(_MAG, a, side="left"), 7)    # first level >= a (or 6)
+    a = np.minimum(np.abs(u), 6.0)
+    hi = np.searchsorted(_MAG, a, side="left")                   # first level >= a
     lo = np.maximum(hi - 1, 0)
     d_hi, d_lo = np.abs(_MAG[hi] - a), np.abs(a - _MAG[lo])
     code = np.where((d_hi < d_lo) | ((d_hi == d_lo) & (hi % 2 == 0)), hi, lo)
