@@ -15,7 +15,8 @@
 //            sigmoid     dl_j += p_j (1 - p_j) s dw_j
 //            normalized  dl_j += u_j s (dw_j - sum_i u_i dw_i)  [(1 - p_j) if sigmoid].
 // Scores are fp32, taken relative to the largest logit they are divided by the sum of, so
-// no row under- or overflows; sums over tokens are fp32 within a lane, fp64 beyond.
+// no row under- or overflows; sums over tokens are fp32 for up to kRun tokens of a lane and fp64
+// beyond, through the scratch memory too.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -151,6 +152,7 @@ __device__ inline bool routed(int id, int n_experts) { return id >= 0 && id < n_
 constexpr int kSumThreads = 1024;
 constexpr int kSumTokens = kSumThreads / kLanes;  // of a workgroup at a time
 constexpr int kMaxGroups = 256;                   // one per compute unit
+constexpr int kRun = 8;                           // tokens that a lane adds in fp32
 
 struct BalanceOut {
   float *loss, *mean_p;
@@ -160,15 +162,20 @@ struct BalanceOut {
 // The experts of one workgroup of the second launch.  Its sums of a group are one cache
 // line (a compute unit has few misses under way: slices of 64 experts, whose sums and
 // counts were two lines each, took 15 us for 256 groups of 256 experts).
-constexpr int kSlice = 16;
+constexpr int kSlice = 8;
+
+struct __attribute__((aligned(128))) SliceSums {
+  double q[kSlice];
+  int32_t n[kSlice];
+};
 
 // A group's sums in scratch, and what the slices of experts add up.
 struct BalanceParts {
-  uint32_t *sums;  // [slices][groups][kSlice sums of q, then kSlice counts]
-  int32_t *t;      // [groups]
-  double *dot;     // [slices]: sum of mean * count
-  int64_t *pairs;  // [slices]
-  uint32_t *done;  // slices that are through (cleared by the sums' launch)
+  SliceSums *sums;  // [slices][groups]
+  int32_t *t;       // [groups]
+  double *dot;      // [slices]: sum of mean * count
+  int64_t *pairs;   // [slices]
+  uint32_t *done;   // slices that are through (cleared by the sums' launch)
 };
 
 // Sums over a wave; every lane has the results, and the same bits.
@@ -212,20 +219,26 @@ __device__ inline void balance_expert(const BalanceOut &o, int e, double p, int3
 
 // A workgroup's share of the tokens.  With ONE workgroup its sums are the result, else its
 // sums of q and its counts go to scratch.  A token's row, and the ids, are fetched a round
-// ahead where the registers hold two rows.  16411 x 256, sigmoid: 9.1 us, vector instructions
-// busy in 57 % of the cycles (17 MB at the copy's rate: 3.4 us).
+// ahead where the registers hold two rows.  Every kRun rounds, and at the end, the lanes' sums
+// go to LDS, 64 of an expert, where kParts threads add a part of them each in fp64.  (fp32
+// sums of a whole batch's tokens are off by 160 2^-24 at 2^24 equal rows, where every addition
+// rounds the same way.)  16411 x 256, sigmoid: 8.7 us (17 MB at the copy's rate: 3.4 us).
 template <bool SIGMOID, int NV, bool VEC, bool ONE>
 __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a, BalanceOut o,
                                                                    BalanceParts parts) {
   constexpr int kWaves = kSumThreads / 64;
-  __shared__ float sums[kWaves][64 * NV];
-  __shared__ int32_t hist[64 * NV];
+  constexpr int kCols = 64 * NV;
+  constexpr int kParts = kSumThreads / kCols;
+  __shared__ __attribute__((aligned(16))) float sums[kSumTokens][kCols];
+  __shared__ double part_sums[kParts][kCols];
+  __shared__ int32_t hist[kCols];
   __shared__ int32_t tokens;
   __shared__ double dot[kWaves];
   __shared__ int64_t all[kWaves];
   const int tid = threadIdx.x;
   const int lane = tid % kLanes, group = tid / kLanes;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSumTokens + group;
+  const int col = tid % kCols, part = tid / kCols;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kSumTokens;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kSumTokens;
   constexpr bool kAhead = NV <= 4;
   Row<NV, VEC> next;
@@ -234,50 +247,67 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a
     next.load(a.logits + t * a.n_experts, a.n_experts, lane);
     if (lane < a.topk) next_id = a.ids[t * a.topk + lane];
   };
-  if (kAhead && first < a.t) fetch(first);
-  for (int e = tid; e < 64 * NV; e += kSumThreads) hist[e] = 0;
+  if (kAhead && base + group < a.t) fetch(base + group);
+  for (int e = tid; e < kCols; e += kSumThreads) hist[e] = 0;
   if (tid == 0) tokens = 0;
   __syncthreads();
   float acc[NV][4] = {};
-  for (int64_t t = first; t < a.t; t += stride) {
-    if (!kAhead) fetch(t);
-    Row<NV, VEC> row = next;
-    const int own_id = next_id;
-    if (kAhead && t + stride < a.t) fetch(t + stride);
-    bool any = routed(own_id, a.n_experts);
-    if (any) atomicAdd(&hist[own_id], 1);
-    for (int j = lane + kLanes; j < a.topk; j += kLanes) {
-      const int id = a.ids[t * a.topk + j];
-      if (!routed(id, a.n_experts)) continue;
-      atomicAdd(&hist[id], 1);
-      any = true;
-    }
-    if (row_max(any ? 1.f : 0.f) == 0.f) continue;  // routed nowhere
-    if (lane == 0) atomicAdd(&tokens, 1);
-    row.clean();
-    float p[NV][4], rest[NV][4];
-    const float inv = row_scores<SIGMOID, NV, VEC>(row, p, rest);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[i][v] += p[i][v] * inv;
-  }
-  // the wave's four tokens, then the waves in order
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      float s = acc[i][v];
-      s += __shfl_xor(s, 16);
-      s += __shfl_xor(s, 32);
-      if (tid % 64 < kLanes) sums[tid / 64][64 * i + 4 * lane + v] = s;
-    }
-  __syncthreads();
   double p = 0.0;
+  // (all threads of the workgroup call)
+  auto join = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      *reinterpret_cast<floatx4 *>(&sums[group][64 * i + 4 * lane]) =
+          floatx4{acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][v] = 0.f;
+    }
+    __syncthreads();
+    constexpr int kRows = kSumTokens / kParts;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) p += static_cast<double>(sums[kRows * part + r][col]);
+  };
+  int run = 0;
+  for (int64_t t0 = base; t0 < a.t; t0 += stride) {
+    const int64_t t = t0 + group;
+    if (t < a.t) {
+      if (!kAhead) fetch(t);
+      Row<NV, VEC> row = next;
+      const int own_id = next_id;
+      if (kAhead && t + stride < a.t) fetch(t + stride);
+      bool any = routed(own_id, a.n_experts);
+      if (any) atomicAdd(&hist[own_id], 1);
+      for (int j = lane + kLanes; j < a.topk; j += kLanes) {
+        const int id = a.ids[t * a.topk + j];
+        if (!routed(id, a.n_experts)) continue;
+        atomicAdd(&hist[id], 1);
+        any = true;
+      }
+      if (row_max(any ? 1.f : 0.f) != 0.f) {  // else routed nowhere
+        if (lane == 0) atomicAdd(&tokens, 1);
+        row.clean();
+        float q[NV][4], rest[NV][4];
+        const float inv = row_scores<SIGMOID, NV, VEC>(row, q, rest);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][v] += q[i][v] * inv;
+      }
+    }
+    if (++run == kRun && t0 + stride < a.t) {
+      join();
+      __syncthreads();  // these reads before the next sums
+      run = 0;
+    }
+  }
+  join();
+  part_sums[part][col] = p;
+  __syncthreads();
+  p = 0.0;
   int32_t c = 0;
   if (tid < a.n_experts) {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) p += static_cast<double>(sums[w][tid]);
+    for (int r = 0; r < kParts; ++r) p += part_sums[r][tid];
     c = hist[tid];
   }
   if constexpr (ONE) {
@@ -291,10 +321,9 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a
     }
   } else {
     if (tid < a.n_experts) {
-      uint32_t *to = parts.sums + ((tid / kSlice) * gridDim.x + blockIdx.x) * (2 * kSlice) +
-                     tid % kSlice;
-      to[0] = __float_as_uint(static_cast<float>(p));
-      to[kSlice] = static_cast<uint32_t>(c);
+      SliceSums &to = parts.sums[(tid / kSlice) * gridDim.x + blockIdx.x];
+      to.q[tid % kSlice] = p;
+      to.n[tid % kSlice] = c;
     }
     if (tid == 0) {
       parts.t[blockIdx.x] = tokens;
@@ -303,10 +332,10 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a
   }
 }
 
-// A workgroup adds the groups' sums of its slice in a fixed order, fp64: thread e + 16 i
-// takes groups i, i + 64, ... of expert e, all on their way at once.  The last workgroup
+// A workgroup adds the groups' sums of its slice in a fixed order, fp64: thread e + 8 i
+// takes groups i and i + 128 of expert e, both on their way at once.  The last workgroup
 // through adds the slices' shares of the loss, a lane each, in a fixed order.  256 groups of
-// 256 experts 7.4 us: latencies, of the lines (from other XCDs' L2), the fence and the counter.
+// 256 experts 6.8 us: latencies, of the lines (from other XCDs' L2), the fence and the counter.
 __global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts parts, int groups,
                                                                    int n_experts, BalanceOut o) {
   constexpr int kParts = kSumThreads / kSlice;
@@ -318,16 +347,15 @@ __global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts 
   const int tid = threadIdx.x;
   const int col = tid % kSlice, part = tid / kSlice;
   const int e = static_cast<int>(blockIdx.x) * kSlice + col;
-  float dp[kAhead];
+  double dp[kAhead];
   int32_t dc[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
     const int g = part + kParts * i;
     const bool in = g < groups && e < n_experts;
-    const uint32_t *from =
-        parts.sums + (static_cast<int>(blockIdx.x) * groups + g) * (2 * kSlice) + col;
-    dp[i] = in ? __uint_as_float(from[0]) : 0.f;
-    dc[i] = in ? static_cast<int32_t>(from[kSlice]) : 0;
+    const SliceSums *from = parts.sums + static_cast<int>(blockIdx.x) * groups + g;
+    dp[i] = in ? from->q[col] : 0.0;
+    dc[i] = in ? from->n[col] : 0;
   }
   const int32_t t = tid < groups ? parts.t[tid] : 0;
   if (tid == 0) st = 0;
@@ -335,10 +363,10 @@ __global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts 
   int32_t c = 0;
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
-    p += static_cast<double>(dp[i]);
+    p += dp[i];
     c += dc[i];
   }
-  // the wave's four parts, then the waves in order
+  // the wave's eight parts, then the waves in order
 #pragma unroll
   for (int x = kSlice; x < 64; x <<= 1) {
     p += __shfl_xor(p, x);
@@ -351,7 +379,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts 
   __syncthreads();
   if (t != 0) atomicAdd(&st, t);
   __syncthreads();
-  if (tid >= 64) return;  // lanes 0 .. 15 of wave 0 have the slice's experts
+  if (tid >= 64) return;  // lanes 0 .. 7 of wave 0 have the slice's experts
   double d = 0.0;
   int64_t n = 0;
   if (part == 0 && e < n_experts) {
@@ -374,7 +402,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_loss_kernel(BalanceParts 
     }
     if (__builtin_amdgcn_readfirstlane(before) + 1 < gridDim.x) return;
     __threadfence();
-    const bool in = tid < static_cast<int>(gridDim.x);  // at most 32 slices
+    const bool in = tid < static_cast<int>(gridDim.x);  // at most 64 slices
     d = in ? __hip_atomic_load(parts.dot + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
     n = in ? __hip_atomic_load(parts.pairs + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
     wave_sums(d, n);
@@ -624,13 +652,14 @@ namespace {
 
 // Scratch: the slices' shares first (16 bytes each), then the groups' sums.
 constexpr size_t kShares = (16 * (kMaxE / kSlice) + 16 + 127) / 128 * 128;
+static_assert(sizeof(SliceSums) == 128 && kMaxE / kSlice <= 64, "a line a group, a lane a slice");
 
 }  // namespace
 
 size_t balance_scratch(int64_t t, int32_t n_experts) {
   const size_t groups = static_cast<size_t>(balance_groups(t));
   const size_t slices = (static_cast<size_t>(n_experts) + kSlice - 1) / kSlice;
-  return groups > 1 ? kShares + groups * (2 * kSlice * slices + 1) * 4 : 0;
+  return groups > 1 ? kShares + groups * (sizeof(SliceSums) * slices + 4) : 0;
 }
 
 hipError_t launch_moe_balance(const BalanceArgs &a, float *loss, int32_t *counts, int32_t *tokens,
@@ -644,9 +673,9 @@ hipError_t launch_moe_balance(const BalanceArgs &a, float *loss, int32_t *counts
     parts.dot = reinterpret_cast<double *>(at);
     parts.pairs = reinterpret_cast<int64_t *>(at + 8 * (kMaxE / kSlice));
     parts.done = reinterpret_cast<uint32_t *>(at + 16 * (kMaxE / kSlice));
-    parts.sums = reinterpret_cast<uint32_t *>(at + kShares);
-    parts.t = reinterpret_cast<int32_t *>(parts.sums) +
-              static_cast<int64_t>(groups) * ((a.n_experts + kSlice - 1) / kSlice) * (2 * kSlice);
+    parts.sums = reinterpret_cast<SliceSums *>(at + kShares);
+    parts.t = reinterpret_cast<int32_t *>(
+        parts.sums + static_cast<int64_t>(groups) * ((a.n_experts + kSlice - 1) / kSlice));
   }
   const bool vec = a.n_experts % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
   by_experts(a.n_experts, vec, [&](auto nv, auto v) {

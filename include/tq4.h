@@ -683,8 +683,8 @@ size_t tq4_moe_balance_workspace_size(int64_t t, int32_t n_experts);
  *   mean_p[e]  = (1 / T) sum over live t of q_te          (0 if T == 0)
  *   loss[0]    = E * sum_e (counts[e] / sum counts) * mean_p[e],  E = n_experts
  * Rows routed nowhere, such as those that fill up a batch, take no part.  An even
- * router has loss 1.  Scores are fp32, sums over tokens fp64 beyond a lane's few;
- * deterministic.
+ * router has loss 1.  Scores are fp32, sums over tokens fp64 beyond runs of at most 8
+ * tokens, for any t; deterministic.
  *   logits   : [t, n_experts] fp32, device;  topk_ids : [t, topk] int32, device
  *   loss, tokens : one value each, counts, mean_p : [n_experts], device, overwritten
  *   workspace: tq4_moe_balance_workspace_size(t, n_experts) bytes, device,

@@ -1,0 +1,78 @@
+"""The router's training step where sums are long or differences cancel.
+
+Bounds, in units U = 2^-24, with X the largest difference of two logits of a row.  A score is
+off by at most (X + 8) of itself, a normalized one by E = 2 X + 20 (test_gpu_balance.py).
+A part of the gradient is r p_e (b_e - sum_i p_i b_i) with r = 1 or 1 - p_e.  It has to be
+right relative to S_e = sum_i p_i |b_e - b_i|, which is what is left of it where b_e and
+the mean are all but equal.  The b are taken relative to a number m near their mean, so
+|b_e - m| <= 2 S_e and sum_i p_i |b_i - m| <= 3 S_e; each difference carries 3 roundings, the
+sum E and 40 roundings (a lane's 32 values and the lanes), the factors E and X + 8:
+2 E + X + 8 + 2 * 3 + 3 (E + 43) <= 11 X + 250.  The mean that m comes from is off by E + 40 of
+the mean magnitude A of the b where they are not integers: 3 roundings of that.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from block_diffusion_lm_tq4_amd import ops  # noqa: F401  (loads libtq4.so)
+    return torch.device("cuda:0")
+
+
+def _ops():
+    from block_diffusion_lm_tq4_amd import ops
+    return ops
+
+
+# ---- sums over tokens ----------------------------------------------------------
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("t,e", [(255, 160), (4096, 160), ((1 << 24) + 5, 5), (1 << 22, 24)])
+def test_equal_logits(dev, t, e, score):
+    """A fresh router's: every addition over tokens rounds the same way.  All probabilities
+    are 1 / E up to 8 roundings of the scores' sum (a lane's values and four joins), the
+    division and the product; a lane adds at most 8 tokens in fp32 and the rest is fp64;
+    the result is rounded once."""
+    o = _ops()
+    l = torch.zeros(t, e, device=dev)
+    ids = (torch.arange(t, device=dev, dtype=torch.int32) % e)[:, None].contiguous()
+    ids[5] = -1
+    loss, counts, tokens, mean = o.moe_balance(l, ids, score=score)
+    assert int(tokens) == t - 1
+    want = torch.bincount(ids[ids >= 0].long(), minlength=e)
+    assert torch.equal(counts.long(), want)
+    assert torch.all((mean.double() * e - 1).abs() <= (8 + 2 + 7 + 1) * U)
+    assert abs(float(loss) - 1) <= (8 + 2 + 7 + 1) * U
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_long_batch_with_rows_routed_nowhere(dev, score):
+    """Whole rounds of a workgroup's tokens are left out, and the last round is part-filled."""
+    o = _ops()
+    t, e = 5 * 16384 + 77, 96
+    g = torch.Generator(device=dev)
+    g.manual_seed(3)
+    l = torch.randn(t, e, generator=g, device=dev)
+    ids = l.topk(3, dim=1).indices.int()
+    ids[16384:3 * 16384] = -1
+    ids[::5] = e
+    loss, counts, tokens, mean = o.moe_balance(l, ids, score=score)
+    live = (ids[:, 0] >= 0) & (ids[:, 0] < e)
+    p = torch.softmax(l[live].double(), 1) if score == "softmax" else torch.sigmoid(l[live].double())
+    want = (p / p.sum(1, keepdim=True)).mean(0)
+    count = torch.bincount(ids[live].flatten().long(), minlength=e)
+    assert int(tokens) == int(live.sum()) and torch.equal(counts.long(), count)
+    x = float(l.max() - l.min()) + 10.0
+    assert torch.all((mean.double() - want).abs() <= (2 * x + 40) * U * want)
+    ref = float(e * (count.double() / count.sum() * want).sum())
+    assert abs(float(loss) - ref) <= (2 * x + 40) * U * ref
