@@ -522,12 +522,12 @@ __device__ inline float gate_part(const RouterGradArgs &g, int64_t t, const Slot
 }
 
 // 16 lanes per token, 16 tokens per workgroup at a time.  A token's row and slots are
-// fetched before anything waits.  16411 x 256, sigmoid, 8 slots: 14.2 us, vector
+// fetched before anything waits.  16411 x 256, sigmoid, 8 slots: 15.2 us, vector
 // instructions busy in 66 % of the cycles (reading and writing alone 8.7).
 template <bool SIGMOID, int NV, bool VEC>
 __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArgs g) {
   __shared__ __attribute__((aligned(16))) float delta_all[kTokens][64 * NV];
-  __shared__ __attribute__((aligned(16))) float share[64 * NV];  // c_e of the loss
+  __shared__ __attribute__((aligned(16))) float share[64 * NV];  // counts, less their mean
   __shared__ int32_t total[kThreads / 64];
   const int tid = threadIdx.x;
   const int lane = tid % kLanes, group = tid / kLanes;
@@ -541,6 +541,7 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
     row.load(g.b.logits + first * n_experts, n_experts, lane);
     own.load(g, first, lane);
   }
+  float unit = 0.f;  // c_e of the loss per pair
   if (has_loss) {
     constexpr int kPer = (64 * NV + kThreads - 1) / kThreads;
     int32_t count[kPer], n = 0;
@@ -558,11 +559,14 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
     n = 0;
     for (int w = 0; w < kThreads / 64; ++w) n += total[w];
     const double pairs = n;
-    const double c0 = pairs > 0.0 && tokens > 0.0 ? dloss * n_experts / (pairs * tokens) : 0.0;
+    unit = pairs > 0.0 && tokens > 0.0
+               ? static_cast<float>(dloss * n_experts / (pairs * tokens))
+               : 0.f;
+    const int mean = n / n_experts;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid + kThreads * i;
-      if (e < 64 * NV) share[e] = static_cast<float>(c0 * count[i]);
+      if (e < 64 * NV) share[e] = static_cast<float>(count[i] - mean);
     }
   }
   __syncthreads();
@@ -589,8 +593,12 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
       for (int j = lane + kLanes; j < g.b.topk; j += kLanes)
         any = any || routed(g.b.ids[t * g.b.topk + j], n_experts);
     const bool live = has_loss && row_max(any ? 1.f : 0.f) > 0.f;
+    // The loss's part: c_e - sum_i q_i c_i = unit * ((n_e - m) - sum_i q_i (n_i - m)) for any
+    // m.  With the row's mean count as m, rounded, so that n_e - m is exact, no term is more than
+    // three times sum_i q_i |c_e - c_i|, and the difference is right relative to that: where one
+    // expert has nearly all the weight the two sides are all but equal.
     floatx4 c[NV];
-    float dot = 0.f;
+    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       c[i] = live ? *reinterpret_cast<const floatx4 *>(share + 64 * i + 4 * lane)
@@ -598,9 +606,19 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         p[i][v] *= inv;
-        dot += p[i][v] * c[i][v];
+        m += p[i][v] * c[i][v];
       }
     }
+    m = __builtin_rintf(row_sum(m));
+    const float of_pair = live ? unit : 0.f;
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        c[i][v] = of_pair * (c[i][v] - m);
+        dot += p[i][v] * c[i][v];
+      }
     dot = row_sum(dot) + taken;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

@@ -76,3 +76,72 @@ def test_a_long_batch_with_rows_routed_nowhere(dev, score):
     assert torch.all((mean.double() - want).abs() <= (2 * x + 40) * U * want)
     ref = float(e * (count.double() / count.sum() * want).sum())
     assert abs(float(loss) - ref) <= (2 * x + 40) * U * ref
+
+
+# ---- differences ---------------------------------------------------------------
+
+def _parts(l, score):
+    """Normalized scores and 1 - p of every row, fp64."""
+    rows = [O.router_scores(r, score) for r in l]
+    q = np.array([r[1] for r in rows])
+    rest = np.array([r[2] for r in rows]) if score == "sigmoid" else np.ones_like(q)
+    return q, rest
+
+
+def _differences(p, b):
+    """p_e (b_e - sum p b) and p_e sum_i p_i |b_e - b_i|, from the differences alone."""
+    d = b[:, :, None] - b[:, None, :]
+    return p * (d * p[:, None, :]).sum(2), p * (np.abs(d) * p[:, None, :]).sum(2)
+
+
+def _loss_gradient(o, dev, l, ids, score, dloss):
+    lg, ig = torch.from_numpy(l).to(dev), torch.from_numpy(ids).to(dev)
+    _, counts, tokens, _ = o.moe_balance(lg, ig, score=score)
+    grad = o.moe_router_backward(lg, ig, score=score, counts=counts, tokens=tokens,
+                                 dloss=torch.full((), dloss, device=dev))
+    n = counts.double().cpu().numpy()
+    c = dloss * len(n) * n / (n.sum() * float(tokens))
+    return grad.double().cpu().numpy(), np.broadcast_to(c, l.shape)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e", [1, 3, 16, 130, 512])
+def test_loss_gradient_of_one_live_expert_is_zero(dev, score, e):
+    o = _ops()
+    rng = np.random.default_rng(e)
+    t = 400
+    l = np.full((t, e), -np.inf, np.float32)
+    at = rng.integers(0, e, t)
+    l[np.arange(t), at] = 3 * rng.standard_normal(t)
+    l[::9] = rng.standard_normal((len(l[::9]), e))       # others keep the counts apart
+    ids = np.argmax(l, axis=1).astype(np.int32)[:, None]
+    grad, _ = _loss_gradient(o, dev, l, ids, score, 0.75)
+    one = np.arange(t) % 9 != 0
+    assert not grad[one].any()
+    if e > 1:
+        assert grad[~one].any()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e", [2, 16, 130, 512])
+@pytest.mark.parametrize("kind", ["dominated", "one count apart", "even", "random"])
+def test_loss_gradient_relative_to_differences(dev, score, e, kind):
+    o = _ops()
+    rng = np.random.default_rng(e)
+    t, reach = 64, 18.0
+    l = rng.uniform(-0.5, 0.5, (t, e)).astype(np.float32)
+    ids = rng.integers(0, e, (t, 1)).astype(np.int32)
+    if kind == "dominated":                              # nearly all the weight on one expert
+        l -= np.float32(4)
+        l[np.arange(t), rng.integers(0, e, t)] += rng.uniform(6, 16, t).astype(np.float32)
+    elif kind == "one count apart":
+        t = 3 * e + 1
+        l = rng.uniform(-0.5, 0.5, (t, e)).astype(np.float32)
+        ids = (np.arange(t) % e).astype(np.int32)[:, None]
+    elif kind == "even":
+        l[:] = 0.25
+    grad, c = _loss_gradient(o, dev, l, ids, score, 0.75)
+    sub = slice(0, 64)
+    q, rest = _parts(l[sub], score)
+    want, size = _differences(q, c[sub])
+    assert np.all(np.abs(grad[sub] - rest * want) <= (11 * reach + 250) * U * rest * size + 1e-36)
