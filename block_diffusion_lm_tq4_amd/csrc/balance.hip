@@ -416,7 +416,8 @@ constexpr int kThreads = 256;
 constexpr int kTokens = kThreads / kLanes;  // of a workgroup at a time
 
 // Slot j of a token as lane j % 16 sees it: its expert (-1: none), that expert's logit and
-// the gate's gradient.
+// the gate's gradient (0 for an expert that is off, whatever stands there: its gate is a constant
+// 0, and 0 times an infinity would spoil the row).
 struct Slot {
   int id;
   float l, d;
@@ -431,6 +432,7 @@ struct Slot {
     if (g.dgates == nullptr) return;
     d = g.dgates[t * g.b.topk + j];
     l = usable(g.b.logits[t * g.b.n_experts + at]);
+    d = l > kOff ? d : 0.f;
   }
 };
 

@@ -703,8 +703,9 @@ int tq4_moe_balance(const float *logits, int64_t t, int32_t n_experts, const int
  * this score, renormalize and scale (tq4_moe_router: softmax, 0, 1), and the loss
  * of tq4_moe_balance, which depends on the logits through mean_p (the counts are
  * constants).  The choice of experts has no gradient.  Slots with an id outside
- * [0, n_experts) contribute nothing; slots of one expert add up; experts that are
- * switched off have gradient 0.
+ * [0, n_experts), or whose expert is switched off, contribute nothing, whatever dgates
+ * holds there; slots of one expert add up; experts that are switched off have
+ * gradient 0.
  *   dgates : [t, topk] fp32, device, or NULL (no gradient from the gates)
  *   counts, tokens : tq4_moe_balance's for these ids, and dloss : one fp32 value,
  *            device; all three, or all NULL (no gradient from the loss)

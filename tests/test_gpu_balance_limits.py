@@ -145,3 +145,34 @@ def test_loss_gradient_relative_to_differences(dev, score, e, kind):
     q, rest = _parts(l[sub], score)
     want, size = _differences(q, c[sub])
     assert np.all(np.abs(grad[sub] - rest * want) <= (11 * reach + 250) * U * rest * size + 1e-36)
+
+
+# ---- slots of experts that are switched off -------------------------------------
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("topk", [3, 20])
+def test_a_slot_whose_expert_is_off_adds_nothing(dev, score, renorm, topk):
+    """Whatever stands in its gradient, an infinity or a NaN too."""
+    o = _ops()
+    rng = np.random.default_rng(topk)
+    t, e = 30, 24
+    l = rng.standard_normal((t, e)).astype(np.float32)
+    l[:, 4] = -np.inf
+    l[:, 5] = np.nan
+    l[7] = -np.inf                                       # a row of only such experts
+    ids = np.argsort(rng.random((t, e)), axis=1)[:, :topk].astype(np.int32)
+    ids[:, 0], ids[:, topk - 1] = 4, 5
+    ids[3, 1] = -1
+    dg = rng.standard_normal((t, topk)).astype(np.float32)
+    off = np.isin(ids, (4, 5)) | (ids < 0)
+    off[7] = True
+    args = dict(score=score, renormalize=renorm, scale=1.5)
+    lg, ig = torch.from_numpy(l).to(dev), torch.from_numpy(ids).to(dev)
+    clean = o.moe_router_backward(lg, ig, torch.from_numpy(np.where(off, 0, dg)).to(dev), **args)
+    assert torch.isfinite(clean).all() and not clean[:, 4:6].any() and not clean[7].any()
+    # three slots leave one, whose renormalized weight is 1 whatever the logits are
+    assert clean.any() == (not renorm or topk > 3)
+    for bad in (np.nan, np.inf, -np.inf, 3e38, 1.0):
+        d = torch.from_numpy(np.where(off, bad, dg).astype(np.float32)).to(dev)
+        assert torch.equal(o.moe_router_backward(lg, ig, d, **args), clean), bad
