@@ -436,20 +436,21 @@ struct Slot {
   }
 };
 
-// The gates' contributions of one token to `delta` (its row of LDS), and what a softmax
-// without renormalization takes from every expert (sum_j p_j a_j).  Lane j of the
-// token takes slots j, j + 16, ...; `own` is its first.
-template <bool SIGMOID>
-__device__ inline float gate_part(const RouterGradArgs &g, int64_t t, const Slot &own, float top,
-                                  float inv, float *delta, int lane) {
+// The gates' contributions of one token to `delta` (its row of LDS): their gradient with respect
+// to the logits, but with SUMS_ONLY (softmax without renormalization) the sums of dw alone.
+// Lane j of the token takes slots j, j + 16, ...; `own` is its first.
+template <bool SIGMOID, bool SUMS_ONLY>
+__device__ inline void gate_part(const RouterGradArgs &g, int64_t t, const Slot &own, float *delta,
+                                 int lane) {
   const int blocks = (g.b.topk + kLanes - 1) / kLanes;
   auto slot = [&](int b) __attribute__((always_inline)) {
     Slot s = own;
     if (b > 0) s.load(g, t, b * kLanes + lane);
     return s;
   };
-  float base = top, norm = inv, mean = 0.f, ref = 0.f;
-  if (g.renormalize) {  // scores relative to the largest chosen one
+  // without renormalization: the scores (sigmoid) themselves
+  float base = 0.f, norm = 1.f, mean = 0.f, ref = 0.f;
+  if (!SUMS_ONLY && g.renormalize) {  // relative to the largest chosen one
     base = kOff;
     for (int b = 0; b < blocks; ++b) base = __builtin_fmaxf(base, slot(b).l);
     base = row_max(base);
@@ -473,19 +474,17 @@ __device__ inline float gate_part(const RouterGradArgs &g, int64_t t, const Slot
     sum = row_sum(sum);
     norm = sum > 0.f ? 1.f / sum : 0.f;
     mean = row_sum(dot) * norm;
-  } else if (SIGMOID) {  // the scores themselves
-    base = 0.f;
-    norm = 1.f;
   }
-  float taken = 0.f;
   for (int b = 0; b < blocks; ++b) {
     const Slot s = slot(b);
     const int id = s.id;
-    float rest = 1.f;
-    const float p = s.l > kOff ? score<SIGMOID>(s.l, base, rest) * norm : 0.f;
-    float add = p * (g.scale * ((s.d - ref) - mean));
-    taken += add;
-    if (SIGMOID) add *= rest;
+    float add = s.d;
+    if constexpr (!SUMS_ONLY) {
+      float rest = 1.f;
+      const float p = s.l > kOff ? score<SIGMOID>(s.l, base, rest) * norm : 0.f;
+      add = p * (g.scale * ((s.d - ref) - mean));
+      if (SIGMOID) add *= rest;
+    }
     // Slots that all have experts of their own, as a router's have, add without a look at
     // each other: a lane leaves its number at its expert and finds it there again.
     if (b == 0) {
@@ -520,7 +519,6 @@ __device__ inline float gate_part(const RouterGradArgs &g, int64_t t, const Slot
     if (first) delta[id] += all;
     wave_lds_fence();
   }
-  return SIGMOID || g.renormalize ? 0.f : row_sum(taken);
 }
 
 // 16 lanes per token, 16 tokens per workgroup at a time.  A token's row and slots are
@@ -536,6 +534,8 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
   const int n_experts = g.b.n_experts;
   const bool has_loss = g.counts != nullptr;
   const bool has_gates = g.dgates != nullptr;
+  // softmax weights as they are: every expert's gradient sees every slot's
+  const bool whole = !SIGMOID && has_gates && !g.renormalize;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kTokens + group;
   Row<NV, VEC> row;
   Slot own;
@@ -581,13 +581,15 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
     row.clean();
     float p[NV][4], rest[NV][4];
     const float inv = row_scores<SIGMOID, NV, VEC>(row, p, rest);
-    float taken = 0.f;
     if (has_gates) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         *reinterpret_cast<floatx4 *>(delta + 64 * i + 4 * lane) = floatx4{0.f, 0.f, 0.f, 0.f};
       wave_lds_fence();
-      taken = gate_part<SIGMOID>(g, t, own, row.top, inv, delta, lane);
+      if (whole)
+        gate_part<SIGMOID, true>(g, t, own, delta, lane);
+      else
+        gate_part<SIGMOID, false>(g, t, own, delta, lane);
     }
     // live: an id in range in any slot
     bool any = own.id >= 0;
@@ -598,9 +600,10 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
     // The loss's part: c_e - sum_i q_i c_i = unit * ((n_e - m) - sum_i q_i (n_i - m)) for any
     // m.  With the row's mean count as m, rounded, so that n_e - m is exact, no term is more than
     // three times sum_i q_i |c_e - c_i|, and the difference is right relative to that: where one
-    // expert has nearly all the weight the two sides are all but equal.
+    // expert has nearly all the weight the two sides are all but equal.  The same with the sums a_e
+    // of the gates' gradients, whose mean need not be rounded.
     floatx4 c[NV];
-    float m = 0.f;
+    float m = 0.f, m_a = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       c[i] = live ? *reinterpret_cast<const floatx4 *>(share + 64 * i + 4 * lane)
@@ -612,21 +615,39 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
       }
     }
     m = __builtin_rintf(row_sum(m));
+    // (`delta` is read where it is used: registers for it would cost a wave per SIMD)
+    auto delta_at = [&](int i) __attribute__((always_inline)) {
+      return *reinterpret_cast<const floatx4 *>(delta + 64 * i + 4 * lane);
+    };
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const floatx4 a = delta_at(i);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) m_a += p[i][v] * a[v];
+      }
+      m_a = row_sum(m_a);
+    }
     const float of_pair = live ? unit : 0.f;
     float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        c[i][v] = of_pair * (c[i][v] - m);
-        dot += p[i][v] * c[i][v];
+      for (int v = 0; v < 4; ++v) c[i][v] = of_pair * (c[i][v] - m);
+      if (whole) {
+        const floatx4 a = delta_at(i);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) c[i][v] += g.scale * (a[v] - m_a);
       }
-    dot = row_sum(dot) + taken;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) dot += p[i][v] * c[i][v];
+    }
+    dot = row_sum(dot);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = 64 * i + 4 * lane;
       floatx4 d = {0.f, 0.f, 0.f, 0.f};
-      if (has_gates) d = *reinterpret_cast<const floatx4 *>(delta + e);
+      if (has_gates && !whole) d = delta_at(i);
 #pragma unroll
       for (int v = 0; v < 4; ++v) d[v] += p[i][v] * rest[i][v] * (c[i][v] - dot);
       float *out = g.dlogits + t * n_experts + e;

@@ -147,6 +147,40 @@ def test_loss_gradient_relative_to_differences(dev, score, e, kind):
     assert np.all(np.abs(grad[sub] - rest * want) <= (11 * reach + 250) * U * rest * size + 1e-36)
 
 
+@pytest.mark.parametrize("e,topk", [(2, 1), (8, 1), (16, 3), (130, 8), (512, 20), (40, 40)])
+@pytest.mark.parametrize("with_loss", [False, True])
+def test_softmax_gates_relative_to_differences(dev, e, topk, with_loss):
+    """Weights that are not renormalized: w_j = s p_j, dl_e = p_e (a_e - sum p a)."""
+    o = _ops()
+    rng = np.random.default_rng(e + topk)
+    t, scale, reach = 60, 2.5, 18.0
+    l = rng.uniform(-0.5, 0.5, (t, e)).astype(np.float32)
+    top = rng.integers(0, e, t)
+    # from even rows to one expert 16 above the others
+    l[np.arange(t), top] += np.linspace(0, 16, t).astype(np.float32)
+    ids = np.argsort(rng.random((t, e)), axis=1)[:, :topk].astype(np.int32)
+    ids[::2, 0] = top[::2]                               # may be in two slots then
+    dg = rng.standard_normal((t, topk)).astype(np.float32)
+    lg, ig, dgg = (torch.from_numpy(v).to(dev) for v in (l, ids, dg))
+    a = np.zeros((t, e))
+    np.add.at(a, (np.arange(t)[:, None], ids), dg.astype(np.float64))
+    b, extra = scale * a, {}
+    p, _ = _parts(l, "softmax")
+    want, size = _differences(p, b)
+    if with_loss:
+        _, counts, tokens, _ = o.moe_balance(lg, ig)
+        extra = dict(counts=counts, tokens=tokens, dloss=torch.full((), 30.0, device=dev))
+        n = counts.double().cpu().numpy()
+        c = np.broadcast_to(30.0 * e * n / (n.sum() * float(tokens)), l.shape)
+        more, size_c = _differences(p, c)
+        want, size = want + more, size + size_c
+    grad = o.moe_router_backward(lg, ig, dgg, scale=scale, **extra).double().cpu().numpy()
+    # sums of up to topk gradients of one expert, and A's own rounding
+    mean = p * (p * np.abs(b)).sum(1, keepdims=True)
+    tol = (11 * reach + 250) * U * size + 3 * U * (2 * reach + 60 + topk) * U * mean
+    assert np.all(np.abs(grad - want) <= tol + 1e-36), np.max(np.abs(grad - want) / (size + 1e-30))
+
+
 # ---- slots of experts that are switched off -------------------------------------
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
