@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][v] += q[i][v] * inv;
+          for (int v = 0; v < 4; ++v) acc[i][v] = __builtin_fmaf(q[i][v], inv, acc[i][v]);
       }
     }
     if (++run == kRun && t0 + stride < a.t) {
@@ -611,7 +611,7 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         p[i][v] *= inv;
-        m += p[i][v] * c[i][v];
+        m = __builtin_fmaf(p[i][v], c[i][v], m);
       }
     }
     m = __builtin_rintf(row_sum(m));
@@ -624,7 +624,7 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
       for (int i = 0; i < NV; ++i) {
         const floatx4 a = delta_at(i);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) m_a += p[i][v] * a[v];
+        for (int v = 0; v < 4; ++v) m_a = __builtin_fmaf(p[i][v], a[v], m_a);
       }
       m_a = row_sum(m_a);
     }
@@ -637,10 +637,10 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
       if (whole) {
         const floatx4 a = delta_at(i);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) c[i][v] += g.scale * (a[v] - m_a);
+        for (int v = 0; v < 4; ++v) c[i][v] = __builtin_fmaf(g.scale, a[v] - m_a, c[i][v]);
       }
 #pragma unroll
-      for (int v = 0; v < 4; ++v) dot += p[i][v] * c[i][v];
+      for (int v = 0; v < 4; ++v) dot = __builtin_fmaf(p[i][v], c[i][v], dot);
     }
     dot = row_sum(dot);
 #pragma unroll
@@ -649,7 +649,10 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
       floatx4 d = {0.f, 0.f, 0.f, 0.f};
       if (has_gates && !whole) d = delta_at(i);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) d[v] += p[i][v] * rest[i][v] * (c[i][v] - dot);
+      for (int v = 0; v < 4; ++v) {
+        const float w = p[i][v] * rest[i][v];
+        d[v] += __builtin_fmaf(w, c[i][v], -(w * dot));
+      }
       float *out = g.dlogits + t * n_experts + e;
       if constexpr (VEC) {
         if (e < n_experts) *reinterpret_cast<floatx4 *>(out) = d;
