@@ -222,7 +222,8 @@ __device__ inline void balance_expert(const BalanceOut &o, int e, double p, int3
 // ahead where the registers hold two rows.  Every kRun rounds, and at the end, the lanes' sums
 // go to LDS, 64 of an expert, where kParts threads add a part of them each in fp64.  (fp32
 // sums of a whole batch's tokens are off by 160 2^-24 at 2^24 equal rows, where every addition
-// rounds the same way.)  16411 x 256, sigmoid: 8.7 us (17 MB at the copy's rate: 3.4 us).
+// rounds the same way.)  16411 x 256, sigmoid: 8.4 us, vector instructions
+// busy in 64 % of the cycles (17 MB at the copy's rate: 3.4 us).
 template <bool SIGMOID, int NV, bool VEC, bool ONE>
 __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(BalanceArgs a, BalanceOut o,
                                                                    BalanceParts parts) {
@@ -522,8 +523,8 @@ __device__ inline void gate_part(const RouterGradArgs &g, int64_t t, const Slot 
 }
 
 // 16 lanes per token, 16 tokens per workgroup at a time.  A token's row and slots are
-// fetched before anything waits.  16411 x 256, sigmoid, 8 slots: 15.2 us, vector
-// instructions busy in 66 % of the cycles (reading and writing alone 8.7).
+// fetched before anything waits.  16411 x 256, sigmoid, 8 slots: 15.3 us, vector
+// instructions busy in 68 % of the cycles (reading and writing alone 8.7).
 template <bool SIGMOID, int NV, bool VEC>
 __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArgs g) {
   __shared__ __attribute__((aligned(16))) float delta_all[kTokens][64 * NV];

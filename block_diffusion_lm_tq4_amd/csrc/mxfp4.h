@@ -20,7 +20,7 @@ hipError_t launch_linear_mxfp4(const uint8_t *xq, const uint8_t *xs, int64_t m, 
                                const uint8_t *wq, const uint8_t *ws, int64_t n, const Tail &tail,
                                void *y, hipStream_t s);
 // The same from bf16 rows in one launch, for the few rows that mxfp4_direct_fits
-// takes; bit-equal.
+// takes; bit-equal where sums are exact (its waves split k).
 bool mxfp4_direct_fits(int64_t m);
 hipError_t launch_linear_mxfp4_direct(const uint16_t *x, int64_t m, int64_t k, const uint8_t *wq,
                                       const uint8_t *ws, int64_t n, const Tail &tail, void *y,

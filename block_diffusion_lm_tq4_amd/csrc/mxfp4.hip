@@ -815,7 +815,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 constexpr int kBufferFlags = 0x00020000;
 
 // TM x TN output tile per workgroup of WM x WN waves, each wave MS x NS
-// 16 x 16 products.  KB bytes (64 or 128, one or two steps) of codes of the tile's TM
+// T x T products.  KB bytes (64 or 128, one or two steps) of codes of the tile's TM
 // activation rows and TN weight rows, and their scale bytes, go to LDS by LDS-direct
 // buffer loads into S stages, S - 1 ahead, with exact load-count waits and one barrier
 // per stage.
@@ -830,12 +830,14 @@ constexpr int kBufferFlags = 0x00020000;
 // every step are as many cache lines to look up as the codes themselves (1024 tokens of
 // 128 experts: 245 us with them, 211 without any).
 //
-// 4096 x 8192 x 2688 in 192 x 256 tiles: 52 us, 3.5 PF; matrix units busy in 48 % of the
-// cycles, the rest loads into LDS; weights straight to registers took 79 to 101.  MoE layer of
-// 128 experts of 1856 x 2688: 16 tokens 46 us up and 39 down (4.4 and 5.3 TB/s of weights),
-// 1024 tokens 96 and 101 (4.8 and 5.2 TB/s with rows that two XCDs read), 4096 tokens 118 and 146
-// (3.8 and 4.7 TB/s with what they write): bound by memory, the up product of 4096 tokens by the
-// one stage on its way, and deeper forms of fewer columns read more and took longer.
+// 4096 x 8192 x 2688 in 192 x 256 tiles: 54 us a call on quantized rows, calls one after
+// another, 3.3 PF (58 of the layer's 74 with bf16 residual and output); matrix units busy in
+// 48 % of the cycles, the rest loads into LDS; weights straight to registers took 79 to 101.  MoE
+// layer of 128 experts of 1856 x 2688: 16 tokens 46 us up and 39 down (4.4 and 5.3 TB/s of
+// weights), 1024 tokens 96 and 101 (4.8 and 5.2 TB/s with rows that two XCDs read), 4096 tokens
+// 118 and 146 (3.8 and 4.7 TB/s with what they write): bound by memory, the up product of 4096
+// tokens by the one stage on its way, and deeper forms of fewer columns read more and took
+// longer.
 //
 // LDS image of a stage: 1 KB pieces of 1024 / KB rows; a row's 16-byte slots
 // are stored at slot ^ key(row).  A 16-byte read takes the wave in phases of 16
@@ -907,10 +909,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(Fp4Args g) {
   } else {
     int i, j;
     if constexpr (TM <= 64) {
-      // Tiles of few rows: their column blocks in a row, over all XCDs.  The rows that every
-      // XCD then reads are small beside the weights, and no XCD gets a tile more than
-      // another (16 tokens 97 us with whole tiles to an XCD, 87 so; 128-row tiles 201 and
-      // 202, 256-row 339 and 347).
+      // Tiles of few rows: their column blocks in a row, over all XCDs.  The rows that every XCD
+      // then reads are small beside the weights, and no XCD gets a tile more than another (16
+      // tokens 97 us with whole tiles to an XCD, 87 so, on other boxes 86 to 96; 128-row tiles
+      // 201 and 202, 256-row 339 and 347).
       i = static_cast<int>(blockIdx.x) / g.tiles_n;
       j = static_cast<int>(blockIdx.x) % g.tiles_n;
     } else {
@@ -1242,10 +1244,12 @@ hipError_t launch_tile(Fp4Args g, int64_t max_tiles, hipStream_t s) {
 // The dense tile: the one with the least time, from the number of tiles and what each
 // kernel was measured to need (us): `alone` a step of 128 k with one workgroup on a compute
 // unit, `each` what every one adds where there are several, `slots` how many fit, `end`
-// a tile's start and stores; 256 compute units.  Fitted to sweeps over m = 64 .. 4096 at
-// (k, n) = (2688, 8192), (8192, 2688) and (1856, 2688), to which the times of the tiles up to
-// 128 x 128 are within 5 % and the largest two's within 18 %; the tile that it gives was
-// the fastest one at all of them.  (Times of the neighbours: 333 x 1856 x 2688 in 32 x 64
+// a tile's start and stores; 256 compute units.  Fitted to sweeps of 11 shapes, m = 64 .. 4096 at
+// (k, n) = (2688, 8192), (8192, 2688) and (1856, 2688), together with 2.5 us of a launch that are
+// left out here, the same for all.  With them the model is off by 3 to 5 % rms for the tiles up to
+// 128 x 128 and by 13 and 18 % for the largest two, whose times it gives up to 27 % too low.  The
+// tile that it gives was the fastest, or as fast, at all 11; other (k, n) were not swept.
+// (Times of the neighbours: 333 x 1856 x 2688 in 32 x 64
 // tiles 6.8 us, 64 x 64 6.1, 64 x 128 8.8; 512 x 2688 x 8192 in 64 x 64 16.9, 128 x 128 13.2,
 // 192 x 256 18.6; 4096 x 2688 x 8192 in 128 x 128 70.4, 192 x 256 67.3, 256 x 256 63.6;
 // 4096 x 8192 x 2688 61.9, 51.7, 52.7.)
@@ -1385,7 +1389,8 @@ hipError_t launch_linear_mxfp4_direct(const uint16_t *x, int64_t m, int64_t k, c
   g.x = x;
   // 32 columns a workgroup where that still gives every compute unit one: the rows are read
   // and quantized half as often (2688 x 8192: one row 5.1 us, 16 rows 7.4, with 16 columns
-  // 5.4 and 9.8; 16 x 4096 x 4096 9.9 and, 16 columns, 8.5; 16 x 8192 x 2688 16.4 and 13.4).
+  // 5.4 and 9.8; 16 x 4096 x 4096 9.9 and, 16 columns, 8.5; 16 x 8192 x 2688 16.4 and 13.4;
+  // nothing was timed for n between 4096 and 8192).
   const int64_t wide = (n + 31) / 32;
   if (wide >= 256)
     hipLaunchKernelGGL((fp4_skinny_kernel<kDense, 2, 16, 1>),
@@ -1438,7 +1443,9 @@ int mxfp4_moe_tile_rows(int64_t pairs, int32_t n_experts, int64_t n1, int64_t k)
 
 // Up to 24 pairs (four tokens of six slots): one to four tokens 14.7, 22.0, 29.9 and 38.9 us,
 // 24 to 25, 28, 33 and 37 to 40 for the batched steps, which are two launches more for the
-// host.
+// host.  That is six slots of 128 experts; an expert that several pairs share is read once for
+// each of them here, and where there are few experts the batched steps read less (5 tokens of
+// 8 experts 24.0).
 bool mxfp4_moe_direct_fits(int64_t t, int32_t topk) {
   return t * topk <= 24 && topk <= kDirectSlots;
 }

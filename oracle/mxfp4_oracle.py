@@ -49,7 +49,7 @@ def mxfp4_rows(v: np.ndarray) -> tuple[np.ndarray, np.ndarray]:
             if not up.any():
                 break
             e = e + step * up
-    e = np.minimum(e, 127)                        # the largest scale: values past 6 * 2^127 become it
+    e = np.minimum(e, 127)                        # the largest scale: what is larger saturates
     u = np.ldexp(np.where(good[..., None], b, 0.0), -e[..., None])
     a = np.minimum(np.abs(u), 6.0)
     hi = np.searchsorted(_MAG, a, side="left")                   # first level >= a
